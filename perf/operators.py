@@ -17,7 +17,9 @@ Cache layout (one row = the head_dim elements of one token and head):
   k_scales u8 [pages, kv_heads, page, d/16] v_scales u8 [pages, kv_heads, d/16, page]
   k_token_scales, v_token_scales f32 [pages, kv_heads, page]
 """
+import functools
 import math
+import operator
 
 import torch
 
@@ -121,24 +123,32 @@ def _nearest(v):
 def _candidate(blocks, amax, s, k):
     """Scales (E4M3 values), codes and values of blocks [..., n, 16] whose maximum maps to k."""
     step = k * s
+    # divisors are tensors throughout: torch multiplies by the rounded reciprocal of a plain number
     e = torch.where(step > 0, amax / step, torch.zeros_like(amax)).clamp(max=448.0)
     e = e.to(torch.float8_e4m3fn).float()
     d = e * s
-    r = torch.where(d > 0, 1.0 / d, torch.zeros_like(d))[..., None]
+    r = torch.where(d > 0, torch.ones_like(d) / d, torch.zeros_like(d))[..., None]
     code = _nearest(blocks.abs() * r)
     c = (_signed_grid(blocks.device)[code.long()] * e[..., None]) * s[..., None]
     return e, code, torch.where(blocks < 0, -c, c)
+
+
+def _error(x, c):
+    """Squared error of each block, summed in element order (the choice between candidates is on it)."""
+    d = x - c
+    return functools.reduce(operator.add, (d * d).unbind(-1))
 
 
 def _nv_rows(x, four_over_six):
     """NVFP4 of FP32 rows [..., d]: nibbles u8 [..., d], E4M3 values [..., d/16], row scales [...]."""
     blocks = x.reshape(*x.shape[:-1], x.shape[-1] // 16, 16)
     amax = blocks.abs().amax(-1)
-    s = amax.amax(-1, keepdim=True) / (1536.0 if four_over_six else 2688.0)
+    top = amax.amax(-1, keepdim=True)
+    s = top / torch.full_like(top, 1536.0 if four_over_six else 2688.0)
     e, code, c = _candidate(blocks, amax, s, 6.0)
     if four_over_six:
         e4, code4, c4 = _candidate(blocks, amax, s, 4.0)
-        four = ((blocks - c4) ** 2).sum(-1) < ((blocks - c) ** 2).sum(-1)
+        four = _error(blocks, c4) < _error(blocks, c)
         e, code = torch.where(four, e4, e), torch.where(four[..., None], code4, code)
     nibble = code | (torch.signbit(blocks).to(torch.uint8) << 3)
     return nibble.reshape(x.shape), e, s[..., 0]
