@@ -19,6 +19,10 @@ Calls (same names as the C ABI):
          res_scales u8 [R, H/32]
   mxfp4_resq_reconstruct(codes, scales, res_codes, res_meta, res_scales,
                          residual) -> f32 [R, H]
+
+The operators that run on the quantized tensors (4-bit linear layers, the
+NVFP4 key/value cache and attention over it) are in rollout.py, C ABI in
+include/fp4q/rollout.h, and exported here under their names.
 """
 import ctypes
 import os
@@ -326,3 +330,11 @@ def nvfp4_quantize_global(x, four_over_six=True, dequant=True, out=None, workspa
                                      _p(scales), _p(ts), _p(dq), _p(workspace), _stream(x))
     _check(st, "nvfp4_quantize_global")
     return codes, scales, ts, dq
+
+
+from . import rollout  # noqa: E402  (uses the helpers above)
+from .rollout import (NvFp4KvCache, mxfp4_linear, nvfp4_kv_append,  # noqa: E402
+                      nvfp4_kv_attention, nvfp4_kv_cache, nvfp4_kv_read, nvfp4_linear,
+                      rollout_lib)
+
+__all__ += rollout.__all__

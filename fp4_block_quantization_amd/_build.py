@@ -1,4 +1,5 @@
-"""Compile the gfx950 HIP library libfp4q.so in-tree (no JIT cache).
+"""Compile the gfx950 HIP libraries libfp4q.so (the quantizer) and
+libfp4q_rollout.so (the rollout engine's operators) in-tree (no JIT cache).
 
 Flags that the bit-exact contract depends on:
   -ffp-contract=off            no FMA contraction of a*b+c
@@ -25,10 +26,15 @@ STANDIN_PATH = os.path.join(BUILD_DIR, "libfp4q_standin.so")
 EXACTDECISION_PATH = os.path.join(BUILD_DIR, "libfp4q_exactdecision.so")
 # K0, the HBM probes (copy, read-only, write-only)
 MEMBENCH_PATH = os.path.join(BUILD_DIR, "libfp4q_membench.so")
+# the rollout engine's operators (include/fp4q/rollout.h)
+ROLLOUT_PATH = os.path.join(BUILD_DIR, "libfp4q_rollout.so")
+CSRC_ROLLOUT = os.path.join(HERE, "csrc_rollout")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["nvfp4.hip", "mxfp4_resq.hip", "fp4q_api.cpp"]
 MEMBENCH_SOURCES = ["membench.hip"]
+ROLLOUT_SOURCES = ["rollout_linear.hip", "rollout_cache.hip", "rollout_attention.hip",
+                   "rollout_api.cpp"]
 
 HIP_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",
@@ -40,10 +46,11 @@ HIP_FLAGS = [
 ]
 
 
-def build(verbose: bool = False, extra_flags=(), out_path: str = None, sources=None) -> str:
-    """Compile the sources (default: the quantizer's) and link libfp4q.so (or
-    out_path, with extra_flags such as -D build knobs); returns the library
-    path."""
+def build(verbose: bool = False, extra_flags=(), out_path: str = None, sources=None,
+          src_dir: str = CSRC) -> str:
+    """Compile the sources (default: the quantizer's) of src_dir and link
+    libfp4q.so (or out_path, with extra_flags such as -D build knobs); returns
+    the library path."""
     out_path = out_path or LIB_PATH
     sources = sources or SOURCES
     obj_dir = os.path.join(os.path.dirname(out_path), "obj_" + os.path.basename(out_path))
@@ -53,7 +60,7 @@ def build(verbose: bool = False, extra_flags=(), out_path: str = None, sources=N
         obj = os.path.join(obj_dir, os.path.splitext(src)[0] + ".o")
         lang = ["-x", "hip"] if src.endswith(".cpp") else []
         cmd = [HIPCC, *HIP_FLAGS, *extra_flags, *lang, "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-               "-c", os.path.join(CSRC, src), "-o", obj]
+               "-c", os.path.join(src_dir, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
@@ -67,11 +74,17 @@ def build(verbose: bool = False, extra_flags=(), out_path: str = None, sources=N
     return out_path
 
 
+def build_rollout(verbose: bool = False) -> str:
+    return build(verbose, out_path=ROLLOUT_PATH, sources=ROLLOUT_SOURCES, src_dir=CSRC_ROLLOUT)
+
+
 def build_all(verbose: bool = False):
-    """libfp4q.so, the stand-in and exact-decision builds and the K0 probes."""
+    """libfp4q.so, its stand-in and exact-decision builds, the K0 probes and
+    libfp4q_rollout.so."""
     return [build(verbose), build(verbose, ["-DFP4Q_STANDIN=1"], STANDIN_PATH),
             build(verbose, ["-DFP4Q_NV_CERTIFY=0"], EXACTDECISION_PATH),
-            build(verbose, out_path=MEMBENCH_PATH, sources=MEMBENCH_SOURCES)]
+            build(verbose, out_path=MEMBENCH_PATH, sources=MEMBENCH_SOURCES),
+            build_rollout(verbose)]
 
 
 if __name__ == "__main__":
