@@ -28,9 +28,12 @@
 // 16 * RT query rows of one cache head (a sequence's queries and the heads
 // that share the cache head; for a prefix, those of all sequences of the
 // group, so that the prefix is read once per 16 * RT of them).  The WAVES
-// wavefronts of a workgroup take tiles in turn and merge their (m, l, O)
-// through LDS; a long context is split over several workgroups, whose
-// partial results a second kernel joins in a fixed order.
+// wavefronts of a workgroup take an item's tiles in turn and merge their
+// (m, l, O) through LDS.  Short contexts take one workgroup per item.  Longer
+// ones are cut into parts of about equal length, one for each workgroup: the
+// part's length follows from the lengths on the device, so that a batch of
+// unequal contexts fills the chip as an equal one does.  A second kernel
+// joins the parts of an item in a fixed order.
 #include "fp4q_device.h"
 #include "rollout_launch.h"
 
@@ -38,12 +41,20 @@ namespace fp4q {
 namespace {
 
 typedef _Float16 half8v __attribute__((ext_vector_type(8)));
+typedef _Float16 half4v __attribute__((ext_vector_type(4)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 typedef int int2v __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr int kTile = 64;  // tokens per step of a wavefront
+
+// Beside the sums of a row's first part: m and l, where the item's further
+// parts are, and how many there are (-1: none, and the output is written).
+struct First {
+  float m, l;
+  int32_t next, more;
+};
 
 struct Params {
   const uint8_t* codes[2];  // keys, values
@@ -57,24 +68,28 @@ struct Params {
   const int32_t* group_offsets;
   uint16_t* out;
   float* lse;
-  float* part_o;   // [splits][rows][D]
-  float2* part_ml; // [splits][rows]
+  // partial results (unscaled sums, and m and l): of an item's first part by query row, for
+  // own items and prefix ones; of further parts by their number and the row of the block
+  float* first_o[2];   // [own, prefix][rows][D]
+  First* first[2];
+  float* next_o;       // [parts][16 * RT][D]
+  float2* next_ml;
   int64_t q_stride, rows;
   int32_t num_pages, page_size, page_groups, kv_heads, per_head;  // per_head: q_heads / kv_heads
   int32_t batch, q_tokens, q_heads, max_pages, max_prefix_pages, groups;
-  int32_t own_blocks, own_splits, prefix_blocks, prefix_splits;
+  int32_t blocks;  // row blocks of a sequence's own items
+  int32_t parts;   // parts to cut all items into, about; 0: one workgroup per item
   float scale;
 };
 
-__device__ __forceinline__ float max_of_halves(float x) {
-  const uint32_t u = __float_as_uint(x);
-  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-__device__ __forceinline__ float max_of_groups(float x) {  // over lanes l, l^16, l^32, l^48
+// Over lanes l, l ^ 16, l ^ 32, l ^ 48: maximum (NaN if one is) and sum.
+__device__ __forceinline__ float max_of_groups(float x) {
   const uint32_t u = __float_as_uint(x);
   const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  return max_of_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+  const uint32_t w = __float_as_uint(
+      __builtin_elementwise_maximum(__uint_as_float(r[0]), __uint_as_float(r[1])));
+  const auto h = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return __builtin_elementwise_maximum(__uint_as_float(h[0]), __uint_as_float(h[1]));
 }
 __device__ __forceinline__ float sum_of_groups(float x) {
   const uint32_t u = __float_as_uint(x);
@@ -103,103 +118,170 @@ __device__ __forceinline__ float factor(float m, float top) {  // 2^(m - top), 0
   return __builtin_amdgcn_exp2f(m - top);
 }
 
-// What a workgroup works on: a block of query rows of one cache head, and
-// the tokens [0, len) of one page-table row.
-struct Job {
+// Lane `from`'s value, for every lane.
+__device__ __forceinline__ int64_t lane_value(int64_t v, int from) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)v, from);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), from);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// An item: a block of query rows of one cache head, and the tokens [0, len)
+// of one page-table row that they see.
+struct Item {
   const int32_t* table;
-  int32_t len;       // tokens any row of the block sees
-  int32_t floor;     // tokens every row of the block sees
-  int32_t first_b;   // row r belongs to sequence first_b + r / (T * per_head)
-  int32_t row0;      // first row of the block, counted from first_b's first
-  int32_t rows;      // rows in the block
-  int32_t own_len;   // own tokens: the limit of row r is own_len - T + 1 + t (prefix: len)
-  int32_t kvh, split, splits, part;  // part: index of this split's partial result
+  int32_t len;      // tokens any row of the block sees
+  int32_t floor;    // tokens every row of the block sees
+  int32_t first_b;  // row r belongs to sequence first_b + (row0 + r) / (T * per_head)
+  int32_t row0;     // first row of the block, counted from first_b's first
+  int32_t rows;     // rows in the block
+  int32_t own_len;  // own tokens: the limit of query t is own_len - T + 1 + t (prefix: len)
+  int32_t kvh;
   bool prefix;
 };
 
-__device__ __forceinline__ int64_t global_row(const Params& p, const Job& j, int r) {
+__device__ __forceinline__ int64_t global_row(const Params& p, const Item& j, int r) {
   const int per_seq = p.q_tokens * p.per_head;
   const int rr = j.row0 + r, b = rr / per_seq, in = rr - b * per_seq;
   const int t = in / p.per_head, g = in - t * p.per_head;
   return ((int64_t)(j.first_b + b) * p.q_tokens + t) * p.q_heads + j.kvh * p.per_head + g;
 }
 
-// The job of workgroup `block`; false: none.  The prefix's workgroups come
-// first (they are the longest), then the sequences' own.
+__device__ __forceinline__ int tiles_of(int len) { return (int)((uint32_t)(len + kTile - 1) / kTile); }
+
+__device__ __forceinline__ int32_t own_length(const Params& p, int b) {
+  return min(max(p.seq_lens[b], 0), p.max_pages * p.page_size);
+}
+
+// Tokens that row block rb of a sequence of own_len tokens sees.
 template <int RB>
-__device__ __forceinline__ bool job_of(const Params& p, int64_t block, Job& j) {
-  const int per_seq = p.q_tokens * p.per_head;
-  const int64_t prefix_jobs = (int64_t)p.prefix_blocks * p.kv_heads * p.prefix_splits;
-  j.prefix = block < prefix_jobs;
-  if (j.prefix) {
-    // row blocks innermost, 8 apart: those of one head and split run together on one of the
-    // 8 dies, whose cache then holds the tokens they share
-    const int64_t pairs = (int64_t)p.kv_heads * p.prefix_splits;
-    const int pair = (int)(block % pairs), slot = (int)(block / pairs);
-    j.kvh = pair / p.prefix_splits;
-    j.split = pair - j.kvh * p.prefix_splits;
-    j.splits = p.prefix_splits;
-    j.part = j.split;
-    // the slot-th row block over all groups: each lane counts one group's blocks
-    const int lane = threadIdx.x % 64;
-    int before = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += 64) {
-      const int g = g0 + lane;
-      int lo = 0, hi = 0;
-      if (g < p.groups) {
-        lo = min(max(p.group_offsets[g], 0), p.batch);
-        hi = min(max(p.group_offsets[g + 1], lo), p.batch);
-      }
-      const int rows = (hi - lo) * per_seq, n = (rows + RB - 1) / RB;
-      int upto = n;
-#pragma unroll
-      for (int s = 1; s < 64; s *= 2) {
-        const int other = __shfl_up(upto, s);
-        if (lane >= s) upto += other;
-      }
-      const uint64_t past = __ballot(before + upto > slot);
-      if (past != 0) {
-        const int at = __builtin_ctzll(past);
-        const int block_in = slot - before - (__shfl(upto, at) - __shfl(n, at));
-        j.first_b = __builtin_amdgcn_readfirstlane(__shfl(lo, at));
-        j.row0 = __builtin_amdgcn_readfirstlane(block_in) * RB;
-        j.rows = min(RB, __builtin_amdgcn_readfirstlane(__shfl(rows, at)) - j.row0);
-        const int group = g0 + at;
-        j.table = p.prefix_table + (int64_t)group * p.max_prefix_pages;
-        j.len = min(max(p.prefix_lens[group], 0), p.max_prefix_pages * p.page_size);
-        j.len = __builtin_amdgcn_readfirstlane(j.len);
-        j.floor = j.own_len = j.len;
-        return true;
-      }
-      before += __shfl(upto, 63);
-    }
-    return false;
+__device__ __forceinline__ int seen_by(const Params& p, int own_len, int rb) {
+  const int last = min((rb + 1) * RB, p.q_tokens * p.per_head) - 1;
+  return max(0, own_len - p.q_tokens + 1 + last / p.per_head);
+}
+
+struct Members {
+  int lo, hi;  // sequences [lo, hi) of a group
+};
+
+__device__ __forceinline__ Members members_of(const Params& p, int g) {
+  Members m;
+  m.lo = min(max(p.group_offsets[g], 0), p.batch);
+  m.hi = min(max(p.group_offsets[g + 1], m.lo), p.batch);
+  return m;
+}
+
+__device__ __forceinline__ int32_t prefix_length(const Params& p, int g) {
+  return min(max(p.prefix_lens[g], 0), p.max_prefix_pages * p.page_size);
+}
+
+// Entries are the groups' prefixes, then the sequences.  An entry's items:
+// f(number of items, tiles of each), row block by row block.  A sequence's
+// item has one tile even if it sees nothing (its zeros have to be written), a
+// prefix's may have none.
+template <int RB, class F>
+__device__ __forceinline__ void items_of(const Params& p, int entry, F f) {
+  if (entry < p.groups) {
+    const Members m = members_of(p, entry);
+    const int rows = (m.hi - m.lo) * p.q_tokens * p.per_head;
+    const int tiles = tiles_of(prefix_length(p, entry));
+    if (tiles > 0) f((rows + RB - 1) / RB * p.kv_heads, tiles);
+    return;
   }
-  block -= prefix_jobs;
-  j.split = (int)(block % p.own_splits);
-  block /= p.own_splits;
-  j.kvh = (int)(block % p.kv_heads);
-  block /= p.kv_heads;
-  const int rb = (int)(block % p.own_blocks);
-  j.first_b = (int)(block / p.own_blocks);
-  j.splits = p.own_splits;
-  j.part = p.prefix_splits + j.split;
-  j.row0 = rb * RB;
-  j.rows = min(RB, per_seq - j.row0);
-  j.table = p.page_table + (int64_t)j.first_b * p.max_pages;
-  j.own_len = min(max(p.seq_lens[j.first_b], 0), p.max_pages * p.page_size);
-  const int first = j.own_len - p.q_tokens + 1;  // the limit of query 0
-  j.len = max(0, first + (j.row0 + j.rows - 1) / p.per_head);
-  j.floor = max(0, first + j.row0 / p.per_head);
-  return true;
+  const int len = own_length(p, entry - p.groups);
+  for (int rb = 0; rb < p.blocks; ++rb) f(p.kv_heads, max(1, tiles_of(seen_by<RB>(p, len, rb))));
+}
+
+// Tiles of a part: an equal share, in whole rounds of four wavefronts, two
+// rounds at least (a shorter part costs more to start than it gives).
+__device__ __forceinline__ int part_tiles(uint32_t total, uint32_t parts) {
+  return (int)max(((total + parts - 1) / parts + 3) / 4 * 4, 8u);
+}
+
+__device__ __forceinline__ int parts_of(int tiles, int share) {
+  return (int)((uint32_t)(tiles + share - 1) / (uint32_t)share);
+}
+
+struct Spot {
+  int entry;           // where a workgroup's part lies; -1: no such part
+  int parts_before;    // parts of the entries before it
+  int further_before;  // of those, the ones that are not an item's first
+  int share;
+};
+
+// The entry of part blockIdx.x.  The workgroup's 256 threads sum the tiles
+// of all entries, which gives the part's length, and then scan the entries'
+// counts of parts.  All sums fit in 31 bits (the host's check).
+template <int RB>
+__device__ __forceinline__ Spot find_part(const Params& p, int (&shared)[16]) {
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int entries = p.groups + p.batch, each = (entries + 255) / 256;
+  const int lo = min(tid * each, entries), hi = min(lo + each, entries);
+  int tiles = 0;
+  for (int e = lo; e < hi; ++e) items_of<RB>(p, e, [&](int n, int each_tiles) { tiles += n * each_tiles; });
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) tiles += __shfl_xor(tiles, s);
+  if (lane == 0) shared[wave] = tiles;
+  __syncthreads();
+  Spot spot;
+  spot.share = part_tiles((uint32_t)(shared[0] + shared[1] + shared[2] + shared[3]),
+                          (uint32_t)p.parts);
+  // counts of parts, and of items
+  int parts = 0, items = 0;
+  auto count = [&](int n, int each_tiles) {
+    parts += n * parts_of(each_tiles, spot.share);
+    items += n;
+  };
+  for (int e = lo; e < hi; ++e) items_of<RB>(p, e, count);
+  int parts_upto = parts, items_upto = items;
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) {
+    const int a = __shfl_up(parts_upto, s), b = __shfl_up(items_upto, s);
+    if (lane >= s) {
+      parts_upto += a;
+      items_upto += b;
+    }
+  }
+  if (lane == 63) {
+    shared[4 + wave] = parts_upto;
+    shared[8 + wave] = items_upto;
+  }
+  if (tid == 0) shared[12] = -1;
+  __syncthreads();
+  int before = parts_upto - parts, items_before = items_upto - items;
+#pragma unroll
+  for (int w = 0; w < 3; ++w) {
+    if (w < wave) {
+      before += shared[4 + w];
+      items_before += shared[8 + w];
+    }
+  }
+  const int want = (int)blockIdx.x;
+  if (want >= before && want < before + parts) {
+    int e = lo;
+    for (;; ++e) {
+      parts = items = 0;
+      items_of<RB>(p, e, count);
+      if (want < before + parts) break;
+      before += parts;
+      items_before += items;
+    }
+    shared[12] = e;
+    shared[13] = before;
+    shared[14] = before - items_before;
+  }
+  __syncthreads();
+  spot.entry = shared[12];
+  spot.parts_before = shared[13];
+  spot.further_before = shared[14];
+  return spot;
 }
 
 template <int D, int RT, int WAVES>
 struct Shared {
-  static constexpr int kVRow = D / 2 + 16;  // padded: neighbouring rows start 16 banks on
+  static constexpr int kVRow = D / 2 + 16;  // padded against bank conflicts
   struct Tile {
     alignas(16) uint8_t codes[kTile * kVRow];
-    alignas(16) uint8_t scales[D / 16][kTile];  // [block][4 (t/4 % 4)][t / 16][t % 4]
+    alignas(16) _Float16 scales[D / 16][4][16];  // [block][t / 4 % 4][t / 16 * 4 + t % 4]
     alignas(16) float k_scale[kTile];
     alignas(16) float v_scale[kTile];
   };
@@ -213,21 +295,26 @@ struct Shared {
   };
 };
 
+// Workgroups of four wavefronts that a CU holds (by registers).
+constexpr int groups_per_cu(int d, int rt) {
+  return rt == 1 ? (d == 64 ? 4 : d == 128 ? 3 : 2) : (d <= 128 ? 2 : 1);
+}
+
+// Tiles [tile_lo, tile_hi) of an item; results to the output (more < 0: the
+// item is whole) or as a partial result (tile_lo 0: by row; else as further
+// part `next`).
 template <int D, int RT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, RT == 2 && D > 128 ? 1 : 2) void attention_kernel(Params p) {
-  constexpr int DT = D / 16, NK = D / 32, KS = D / 64, VL = D / 32;
-  constexpr int EU = (DT * 8 + 63) / 64;  // 8-token pieces of value scales per lane
+__device__ __forceinline__ void attend(const Params& p, const Item& job, int tile_lo, int tile_hi,
+                                       int next_part, int more, Shared<D, RT, WAVES>& sh) {
+  constexpr int DT = D / 16, NK = D / 32, KS = D / 64;
+  constexpr int KSW = KS == 3 ? 2 : 1;
+  constexpr int VA = D / 128;          // 16-byte pieces of 16 tokens' value codes per lane,
+  constexpr bool VB = D % 128 != 0;    // and one of 8 bytes
+  constexpr int kVRow = Shared<D, RT, WAVES>::kVRow;
   constexpr int RB = 16 * RT;
-  __shared__ Shared<D, RT, WAVES> sh;
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int col = lane % 16, grp = lane / 16;
-  Job job;
-  if (!job_of<RB>(p, blockIdx.x, job)) return;
-
-  const int tiles = (job.len + kTile - 1) / kTile;
-  const int tile_lo = (int)((int64_t)tiles * job.split / job.splits);
-  const int tile_hi = (int)((int64_t)tiles * (job.split + 1) / job.splits);
-  const int steps = max(0, (tile_hi - tile_lo - wave + WAVES - 1) / WAVES);
+  const int steps = max(0, min(tile_hi, tiles_of(job.len)) - tile_lo - wave + WAVES - 1) / WAVES;
   const int last_group = (job.len - 1) / 16;
 
   // queries: lane (col, grp) holds row col's elements [grp * D/4, (grp + 1) * D/4)
@@ -260,7 +347,9 @@ __global__ __launch_bounds__(64 * WAVES, RT == 2 && D > 128 ? 1 : 2) void attent
     const int field = (int)(top >> 7);
     const int ex = top == 0 || field == 255 ? 0 : 14 + 127 - max(field, 1);
     const float sign = p.scale < 0.0f ? -1.0f : 1.0f;
-    c_q[rt] = __builtin_ldexpf(__builtin_fabsf(p.scale) * kLog2e, -ex);
+    // (never 0, so that a masked score's -infinity stays one)
+    c_q[rt] = p.scale == 0.0f ? 0x1p-149f
+                              : __builtin_ldexpf(__builtin_fabsf(p.scale) * kLog2e, -ex);
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
       const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
@@ -284,120 +373,133 @@ __global__ __launch_bounds__(64 * WAVES, RT == 2 && D > 128 ? 1 : 2) void attent
   // value scales up to `bound` times `norm` reach 2^15
   float bound = 0.0f, norm = 1.0f;
 
-  // Pages: lane 4 k + j holds the place of the 16 tokens j of step 16 n + k.
-  int64_t page_head = 0;  // page * kv_heads + head
-  int32_t page_at = 0;    // first token's place in the page
+  // Pages: lane 4 k + j holds, for the 16 tokens j of step 16 n + k, the index of their first
+  // cache row and of their first byte among the value scales of block 0.
+  int64_t page_row = 0, page_scale = 0;
   auto load_pages = [&](int first_step) {
     const int tile = tile_lo + wave + (first_step + lane / 4) * WAVES;
     const int g = min(tile * 4 + lane % 4, last_group);
-    const int page = g / p.page_groups;
+    const int page = g / p.page_groups, at = (g - page * p.page_groups) * 16;
     const int id = min(max(job.table[page], 0), p.num_pages - 1);
-    page_head = (int64_t)id * p.kv_heads + job.kvh;
-    page_at = (g - page * p.page_groups) * 16;
+    const int64_t head = ((int64_t)id * p.kv_heads + job.kvh) * p.page_size;
+    page_row = head + at;
+    page_scale = head * DT + at;
   };
-  int64_t at_ph[4];  // of the step being loaded: page and head, and place, of its 16-token groups
-  int32_t at_place[4];
+  int64_t row[4], vscale[4];  // of the step being loaded
   auto locate = [&](int step) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int from = (step % 16) * 4 + j;
-      at_ph[j] = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)page_head, from) |
-                              (uint64_t)(uint32_t)__builtin_amdgcn_readlane(
-                                  (int)(page_head >> 32), from)
-                                  << 32);
-      at_place[j] = __builtin_amdgcn_readlane(page_at, from);
+      row[j] = lane_value(page_row, from);
+      vscale[j] = lane_value(page_scale, from);
     }
   };
-#define FP4Q_PICK(v, j) ((j) == 0 ? v[0] : (j) == 1 ? v[1] : (j) == 2 ? v[2] : v[3])
 
-  uint32_t kw[4][NK];     // key codes: token 16 j + col, elements grp * D/4 ...
-  uint32_t ks[4];         // their block scales
-  u32x4v vw[VL];          // value codes, 16-byte pieces in memory order
-  u32x2v ve[EU];          // value block scales, 8 tokens each
+  // A lane's share of the 16 tokens j: 16 bytes of value codes (8 for 64-element heads; 192:
+  // 16 and 8), one word of value scales (4 tokens of a block), and the key codes of token col
+  // that its queries' elements meet.  Loaded through descriptors at the 16 tokens' first byte:
+  // the lane's offset never changes, so a load takes no address arithmetic, and one past the
+  // last step takes an empty descriptor instead of a branch.
+  uint32_t kw[4][NK], ve[4];
+  uint32_t ks[4][KSW];  // the words that hold the lane's KS key scale bytes
+  u32x4v vw[4][VA ? VA : 1];
+  u32x2v vh[4];
   float kt = 0.0f, vt = 0.0f;
-  auto load_values = [&]() {
-    int64_t row[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) row[j] = at_ph[j] * p.page_size + at_place[j];
-#pragma unroll
-    for (int r = 0; r < VL; ++r) {
-      const int piece = r * 64 + lane, t = piece / VL, in = piece - t * VL;
-      vw[r] = *(const u32x4v*)(p.codes[1] + (FP4Q_PICK(row, t / 16) + t % 16) * (D / 2) + in * 16);
-    }
-#pragma unroll
-    for (int r = 0; r < EU; ++r) {
-      const int u = r * 64 + lane, dt = u / 8, j = u / 2 % 4;
-      const int64_t at = FP4Q_PICK(at_place, j) + u % 2 * 8;
-      if (DT * 8 % 64 == 0 || u < DT * 8)
-        ve[r] = *(const u32x2v*)(p.scales[1] + (FP4Q_PICK(at_ph, j) * DT + dt) * p.page_size + at);
-    }
-    const int64_t mine = FP4Q_PICK(row, lane / 16) + col;
-    kt = p.token_scales[0][mine];
-    vt = p.token_scales[1][mine];
-  };
-  auto load_keys = [&]() {
+  const uint32_t e_lane = (uint32_t)min(lane, DT * 4 - 1);
+  const uint32_t e_at = e_lane / 4 * p.page_size + e_lane % 4 * 4;
+  const uint32_t key_at = (uint32_t)(col * (D / 2) + grp * (D / 8));
+  const uint32_t key_scale_word = KSW == 2 ? grp / 2 * 4 : grp * KS / 4 * 4;
+  const uint32_t key_scale_at = (uint32_t)(col * DT) + key_scale_word;
+  const uint32_t key_scale_shift = 8 * (grp * KS - key_scale_word);
+  auto load_values = [&](int step) {
+    const int bytes = __builtin_amdgcn_readfirstlane(step < steps ? -1 : 0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t row = at_ph[j] * p.page_size + at_place[j] + col;
-      const uint8_t* src = p.codes[0] + row * (D / 2) + grp * (D / 8);
+      const auto c = __builtin_amdgcn_make_buffer_rsrc((void*)(p.codes[1] + row[j] * (D / 2)), 0,
+                                                       bytes, 0x20000);
+      const auto e =
+          __builtin_amdgcn_make_buffer_rsrc((void*)(p.scales[1] + vscale[j]), 0, bytes, 0x20000);
+#pragma unroll
+      for (int r = 0; r < VA; ++r)
+        vw[j][r] = __builtin_amdgcn_raw_buffer_load_b128(c, lane * 16, r * 1024, 0);
+      if constexpr (VB) vh[j] = __builtin_amdgcn_raw_buffer_load_b64(c, lane * 8, VA * 1024, 0);
+      ve[j] = __builtin_amdgcn_raw_buffer_load_b32(e, e_at, 0, 0);
+    }
+    if (step < steps) {
+      const int from = step % 16 * 4 + grp;  // the lane that holds this lane's tokens' place
+      const int64_t mine = __shfl(page_row, from) + col;
+      kt = p.token_scales[0][mine];
+      vt = p.token_scales[1][mine];
+    }
+  };
+  auto load_keys = [&](int step) {
+    const int bytes = __builtin_amdgcn_readfirstlane(step < steps ? -1 : 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const auto c = __builtin_amdgcn_make_buffer_rsrc((void*)(p.codes[0] + row[j] * (D / 2)), 0,
+                                                       bytes, 0x20000);
+      const auto e =
+          __builtin_amdgcn_make_buffer_rsrc((void*)(p.scales[0] + row[j] * DT), 0, bytes, 0x20000);
       if constexpr (NK % 4 == 0) {
 #pragma unroll
         for (int k = 0; k < NK; k += 4) {
-          const uint4 w = *(const uint4*)(src + k * 4);
-          kw[j][k] = w.x, kw[j][k + 1] = w.y, kw[j][k + 2] = w.z, kw[j][k + 3] = w.w;
+          const u32x4v w = __builtin_amdgcn_raw_buffer_load_b128(c, key_at, k * 4, 0);
+          kw[j][k] = w[0], kw[j][k + 1] = w[1], kw[j][k + 2] = w[2], kw[j][k + 3] = w[3];
         }
       } else {
 #pragma unroll
         for (int k = 0; k < NK; k += 2) {
-          const uint2 w = *(const uint2*)(src + k * 4);
-          kw[j][k] = w.x, kw[j][k + 1] = w.y;
+          const u32x2v w = __builtin_amdgcn_raw_buffer_load_b64(c, key_at, k * 4, 0);
+          kw[j][k] = w[0], kw[j][k + 1] = w[1];
         }
       }
-      const uint8_t* sc = p.scales[0] + row * DT + grp * KS;
-      if constexpr (KS == 4)
-        ks[j] = *(const uint32_t*)sc;
-      else if constexpr (KS == 2)
-        ks[j] = *(const uint16_t*)sc;
-      else if constexpr (KS == 1)
-        ks[j] = *sc;
-      else
-        ks[j] = sc[0] | sc[1] << 8 | sc[2] << 16;
+      // whole words: a byte or half-word load would be widened, and so waited for, at once
+      if constexpr (KSW == 1) {
+        ks[j][0] = __builtin_amdgcn_raw_buffer_load_b32(e, key_scale_at, 0, 0);
+      } else {
+        const u32x2v w = __builtin_amdgcn_raw_buffer_load_b64(e, key_scale_at, 0, 0);
+        ks[j][0] = w[0], ks[j][1] = w[1];
+      }
     }
   };
 
-#undef FP4Q_PICK
-
   auto& tile = sh.tile[wave];
+  const int turned = 16 * (col / 4) + 4 * grp + col % 4;  // the token whose row this lane names
+  auto turned_codes = [&](int dt) {
+    return __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+        (__attribute__((address_space(3))) int2v*)(tile.codes + turned * kVRow + dt * 8));
+  };
   if (steps > 0) {
     load_pages(0);
     locate(0);
-    load_values();
-    load_keys();
+    load_values(0);
+    load_keys(0);
   }
   for (int step = 0; step < steps; ++step) {
     const int t0 = (tile_lo + wave + step * WAVES) * kTile;
     const int left = job.len - t0;  // tokens of this tile that exist
     // values and scales into LDS; scales of tokens past the end become zero, so that
     // whatever lies there adds nothing
+    if (left < kTile) {
 #pragma unroll
-    for (int r = 0; r < VL; ++r) {
-      const int piece = r * 64 + lane, t = piece / VL, in = piece - t * VL;
-      *(u32x4v*)(tile.codes + t * Shared<D, RT, WAVES>::kVRow + in * 16) = vw[r];
+      for (int j = 0; j < 4; ++j) {
+        const int n = min(max(left - 16 * j - 4 * (int)(e_lane % 4), 0), 4);  // of these 4 tokens
+        ve[j] = n == 0 ? 0 : ve[j] & (~0u >> (32 - 8 * n));
+      }
     }
 #pragma unroll
-    for (int r = 0; r < EU; ++r) {
-      const int u = r * 64 + lane, dt = u / 8, j = u / 2 % 4, half = u % 2;
-      u32x2v e = ve[r];
-      if (left < kTile) {
-        const int n = min(max(left - 16 * j - 8 * half, 0), 8);  // of these 8 tokens
-        const uint64_t keep = n == 0 ? 0 : ~(uint64_t)0 >> (64 - 8 * n);
-        e.x &= (uint32_t)keep;
-        e.y &= (uint32_t)(keep >> 32);
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int r = 0; r < VA; ++r) {
+        const int byte = r * 1024 + lane * 16;
+        *(u32x4v*)(tile.codes + (16 * j + byte / (D / 2)) * kVRow + byte % (D / 2)) = vw[j][r];
       }
-      if (DT * 8 % 64 == 0 || u < DT * 8) {
-        *(uint32_t*)&tile.scales[dt][(2 * half) * 16 + j * 4] = e.x;
-        *(uint32_t*)&tile.scales[dt][(2 * half + 1) * 16 + j * 4] = e.y;
+      if constexpr (VB) {
+        const int byte = VA * 1024 + lane * 8;
+        *(u32x2v*)(tile.codes + (16 * j + byte / (D / 2)) * kVRow + byte % (D / 2)) = vh[j];
       }
+      const half2v a = e4m3_f16x2<0>(ve[j]), b = e4m3_f16x2<1>(ve[j]);
+      *(half4v*)&tile.scales[e_lane / 4][e_lane % 4][j * 4] = (half4v){a[0], a[1], b[0], b[1]};
     }
     const float vt_live = lane < left ? vt : 0.0f;
     if (__any(vt_live > bound)) {
@@ -418,11 +520,9 @@ __global__ __launch_bounds__(64 * WAVES, RT == 2 && D > 128 ? 1 : 2) void attent
     }
     tile.k_scale[lane] = kt;
     tile.v_scale[lane] = vt_live * norm;
-    if (step + 1 < steps) {
-      if ((step + 1) % 16 == 0) load_pages(step + 1);
-      locate(step + 1);
-      load_values();
-    }
+    if ((step + 1) % 16 == 0) load_pages(step + 1);
+    locate(step + 1);
+    load_values(step + 1);
 
     // scores
     float4v s[RT][4];
@@ -430,7 +530,12 @@ __global__ __launch_bounds__(64 * WAVES, RT == 2 && D > 128 ? 1 : 2) void attent
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) s[rt][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
-      const half2v e01 = e4m3_f16x2<0>(ks[j]), e23 = e4m3_f16x2<1>(ks[j]);
+      uint32_t e_bytes = ks[j][0];
+      if constexpr (KSW == 2)
+        e_bytes = (uint32_t)(((uint64_t)ks[j][1] << 32 | ks[j][0]) >> key_scale_shift);
+      else if constexpr (KS < 4)
+        e_bytes >>= key_scale_shift;
+      const half2v e01 = e4m3_f16x2<0>(e_bytes), e23 = e4m3_f16x2<1>(e_bytes);
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
         const int b = k / 2;  // 16-element block of the lane's range
@@ -443,7 +548,7 @@ __global__ __launch_bounds__(64 * WAVES, RT == 2 && D > 128 ? 1 : 2) void attent
             s[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[rt][k], s[rt][j], 0, 0, 0);
       }
     }
-    if (step + 1 < steps) load_keys();
+    load_keys(step + 1);
 
     // softmax
     half8v w[RT][2];
@@ -451,22 +556,27 @@ __global__ __launch_bounds__(64 * WAVES, RT == 2 && D > 128 ? 1 : 2) void attent
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       if (rt > 0 && rt * 16 >= job.rows) continue;
-      float top = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4v sc = *(const float4v*)&tile.k_scale[16 * j + 4 * grp];
-        s[rt][j] *= sc;
-        if (edge) {
+      for (int j = 0; j < 4; ++j) s[rt][j] *= *(const float4v*)&tile.k_scale[16 * j + 4 * grp];
+      if (edge) {
+        asm volatile("");  // keeps this a branch: most tiles have no edge
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (t0 + 16 * j + 4 * grp + i >= limit[rt]) s[rt][j][i] = -INFINITY;
-        }
-        top = fmaxf(top, fmaxf(fmaxf(s[rt][j][0], s[rt][j][1]), fmaxf(s[rt][j][2], s[rt][j][3])));
       }
-      top = max_of_groups(top);
-      top = top == -INFINITY ? top : top * c_q[rt];
-      if (__any(top > m[rt])) {
-        const float grown = fmaxf(m[rt], top);
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        top = __builtin_elementwise_maximum(
+            __builtin_elementwise_maximum(top, s[rt][j][0]), s[rt][j][1]);
+        top = __builtin_elementwise_maximum(
+            __builtin_elementwise_maximum(top, s[rt][j][2]), s[rt][j][3]);
+      }
+      top = max_of_groups(top) * c_q[rt];
+      if (__any(!(top <= m[rt]))) {
+        const float grown = __builtin_elementwise_maximum(m[rt], top);
         const float keep = m[rt] == -INFINITY ? 1.0f : factor(m[rt], grown);
         m[rt] = grown;
         l[rt] *= keep;
@@ -476,46 +586,50 @@ __global__ __launch_bounds__(64 * WAVES, RT == 2 && D > 128 ? 1 : 2) void attent
       const float base = m[rt] == -INFINITY ? 0.0f : m[rt];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4v sc = *(const float4v*)&tile.v_scale[16 * j + 4 * grp];
         float4v e;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][j][i], c_q[rt], -base));
-          if (edge && t0 + 16 * j + 4 * grp + i >= limit[rt]) e[i] = 0.0f;
           l[rt] += e[i];
         }
-        e *= sc;
+        e *= *(const float4v*)&tile.v_scale[16 * j + 4 * grp];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[rt][j / 2][j % 2 * 4 + i] = (_Float16)e[i];
       }
     }
 
-    // values
-    const int turned = 16 * (col / 4) + 4 * grp + col % 4;  // the token whose row this lane names
+    // values, the next 16 columns' codes and scales read while these are multiplied
+    int2v c = turned_codes(0);
+    half8v e0 = *(const half8v*)&tile.scales[0][grp][0], e1 = *(const half8v*)&tile.scales[0][grp][8];
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) {
-      const int2v c = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-          (__attribute__((address_space(3))) int2v*)(tile.codes +
-                                                     turned * Shared<D, RT, WAVES>::kVRow +
-                                                     dt * 8));
-      const uint4 e = *(const uint4*)&tile.scales[dt][grp * 16];
-      const half8v v0 = decode8((uint32_t)c[0], e4m3_f16x2<0>(e.x), e4m3_f16x2<1>(e.x),
-                                e4m3_f16x2<0>(e.y), e4m3_f16x2<1>(e.y));
-      const half8v v1 = decode8((uint32_t)c[1], e4m3_f16x2<0>(e.z), e4m3_f16x2<1>(e.z),
-                                e4m3_f16x2<0>(e.w), e4m3_f16x2<1>(e.w));
+      int2v c_next = c;
+      half8v e0_next = e0, e1_next = e1;
+      if (dt + 1 < DT) {
+        c_next = turned_codes(dt + 1);
+        e0_next = *(const half8v*)&tile.scales[dt + 1][grp][0];
+        e1_next = *(const half8v*)&tile.scales[dt + 1][grp][8];
+      }
+      const half8v v0 = decode8((uint32_t)c[0], (half2v){e0[0], e0[1]}, (half2v){e0[2], e0[3]},
+                                (half2v){e0[4], e0[5]}, (half2v){e0[6], e0[7]});
+      const half8v v1 = decode8((uint32_t)c[1], (half2v){e1[0], e1[1]}, (half2v){e1[2], e1[3]},
+                                (half2v){e1[4], e1[5]}, (half2v){e1[6], e1[7]});
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         if (rt > 0 && rt * 16 >= job.rows) continue;
         o[rt][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w[rt][0], o[rt][dt], 0, 0, 0);
         o[rt][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w[rt][1], o[rt][dt], 0, 0, 0);
       }
+      c = c_next;
+      e0 = e0_next;
+      e1 = e1_next;
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
   // the wavefronts' results joined, 16 rows at a time; each thread takes pairs of one row
   const float unscale = bound == 0.0f ? 0.0f : 1.0f / norm;
   const int tid = threadIdx.x, row_in = tid / (WAVES * 4), sub = tid % (WAVES * 4);
-  const bool direct = p.part_o == nullptr;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     if (rt * 16 >= job.rows) break;
@@ -538,6 +652,8 @@ __global__ __launch_bounds__(64 * WAVES, RT == 2 && D > 128 ? 1 : 2) void attent
         total += f[w] * sh.merge.ml[w][row_in].y;
       }
       const int64_t row = global_row(p, job, r);
+      const int64_t next = (int64_t)next_part * RB + r;
+      float* to = tile_lo > 0 ? p.next_o + next * D : p.first_o[job.prefix] + row * D;
       const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
       for (int c = 0; c < D / (WAVES * 8); ++c) {
@@ -549,33 +665,156 @@ __global__ __launch_bounds__(64 * WAVES, RT == 2 && D > 128 ? 1 : 2) void attent
           a = __builtin_fmaf(f[w], v.x, a);
           b = __builtin_fmaf(f[w], v.y, b);
         }
-        if (direct)
+        if (more < 0)
           *(uint32_t*)(p.out + row * D + d) = cvt_bf16x2(a * inv, b * inv);
         else
-          *(float2*)(p.part_o + ((int64_t)job.part * p.rows + row) * D + d) = make_float2(a, b);
+          *(float2*)(to + d) = make_float2(a, b);
       }
       if (sub == 0) {
-        if (!direct)
-          p.part_ml[(int64_t)job.part * p.rows + row] = make_float2(top, total);
-        else if (p.lse)
+        if (tile_lo > 0)
+          p.next_ml[next] = make_float2(top, total);
+        else if (p.parts > 0)
+          p.first[job.prefix][row] = First{top, total, next_part, more};
+        if (more < 0 && p.lse)
           p.lse[row] = total == 0.0f ? -INFINITY : (base + __builtin_log2f(total)) * kLn2;
       }
     }
   }
 }
 
-// The partial results of one query row joined, in the order of their tokens:
-// prefix, then own.  D / 4 threads per row.
-template <int D>
+template <int RB>
+__device__ __forceinline__ void own_item(const Params& p, int b, int rb, Item& j) {
+  j.prefix = false;
+  j.first_b = b;
+  j.row0 = rb * RB;
+  j.rows = min(RB, p.q_tokens * p.per_head - j.row0);
+  j.table = p.page_table + (int64_t)b * p.max_pages;
+  j.own_len = own_length(p, b);
+  j.len = seen_by<RB>(p, j.own_len, rb);
+  j.floor = max(0, j.own_len - p.q_tokens + 1 + j.row0 / p.per_head);
+}
+
+// The same value in every lane, said so: descriptors and branches come from it.
+__device__ __forceinline__ int32_t same(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ void make_uniform(Item& j) {
+  j.len = same(j.len);
+  j.floor = same(j.floor);
+  j.first_b = same(j.first_b);
+  j.row0 = same(j.row0);
+  j.rows = same(j.rows);
+  j.own_len = same(j.own_len);
+  j.kvh = same(j.kvh);
+}
+
+// One workgroup per own item.
+template <int D, int RT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, groups_per_cu(D, RT) * 4 / WAVES > 0
+                                             ? (groups_per_cu(D, RT) * 4 / WAVES) * WAVES / 4
+                                             : WAVES / 4) void attention_items(Params p) {
+  __shared__ Shared<D, RT, WAVES> sh;
+  const uint32_t block = blockIdx.x, pair = block / (uint32_t)p.kv_heads;
+  Item job;
+  own_item<16 * RT>(p, (int)(pair / (uint32_t)p.blocks), (int)(pair % (uint32_t)p.blocks), job);
+  job.kvh = (int)(block % (uint32_t)p.kv_heads);
+  make_uniform(job);
+  attend<D, RT, WAVES>(p, job, 0, tiles_of(job.len), 0, -1, sh);
+}
+
+// One workgroup per part.
+template <int D, int RT>
+__global__ __launch_bounds__(256, groups_per_cu(D, RT)) void attention_parts(Params p) {
+  constexpr int RB = 16 * RT;
+  __shared__ Shared<D, RT, 4> sh;
+  __shared__ int scratch[16];
+  const Spot spot = find_part<RB>(p, scratch);
+  const int entry = same(spot.entry), share = same(spot.share);
+  if (entry < 0) return;
+  int at = (int)blockIdx.x - same(spot.parts_before);  // the part's number in its entry
+  int further = same(spot.further_before);
+  Item job;
+  int tiles, item, n;
+  if (entry < p.groups) {
+    const Members m = members_of(p, entry);
+    const int rows = (m.hi - m.lo) * p.q_tokens * p.per_head, blocks = (rows + RB - 1) / RB;
+    job.prefix = true;
+    job.table = p.prefix_table + (int64_t)entry * p.max_prefix_pages;
+    job.len = job.floor = job.own_len = prefix_length(p, entry);
+    tiles = tiles_of(job.len);
+    n = parts_of(tiles, share);
+    item = at / n;
+    // heads outside, row blocks inside: a head's blocks share their tokens
+    job.kvh = item / blocks;
+    job.first_b = m.lo;
+    job.row0 = (item - job.kvh * blocks) * RB;
+    job.rows = min(RB, rows - job.row0);
+  } else {
+    int rb = 0;
+    for (;; ++rb) {
+      own_item<RB>(p, entry - p.groups, rb, job);
+      tiles = max(1, tiles_of(job.len));
+      n = parts_of(tiles, share);
+      if (at < n * p.kv_heads) break;
+      at -= n * p.kv_heads;
+      further += (n - 1) * p.kv_heads;
+    }
+    item = job.kvh = at / n;
+  }
+  make_uniform(job);
+  tiles = same(tiles);
+  n = same(n);
+  item = same(item);
+  const int part = at - item * n;
+  further += item * (n - 1);
+  // n parts of equal length, to a tile
+  const int lo = same((int)((int64_t)tiles * part / n));
+  const int hi = same((int)((int64_t)tiles * (part + 1) / n));
+  attend<D, RT, 4>(p, job, lo, hi, further + max(part - 1, 0),
+                   p.groups == 0 && n == 1 ? -1 : n - 1, sh);
+}
+
+// The partial results of query rows joined, in the order of their tokens:
+// prefix, then own.  A workgroup takes ROWS heads of one token (1, or all
+// that its threads have room for); D / 4 threads hold a row's elements, and
+// with ROWS 1 the others share the row's parts.
+template <int D, int RT, bool ONE>
 __global__ __launch_bounds__(256) void attention_join(Params p) {
-  constexpr int PER = 256 / (D / 4);
-  const int64_t row = (int64_t)blockIdx.x * PER + threadIdx.x / (D / 4);
-  if (threadIdx.x / (D / 4) >= PER || row >= p.rows) return;
-  const int d = threadIdx.x % (D / 4) * 4;
-  int first = p.prefix_splits;
+  constexpr int RB = 16 * RT, COLS = D / 4, LANES = 256 / COLS;
+  __shared__ float4v acc_of[LANES][COLS];
+  __shared__ float top_of[LANES], total_of[LANES];
+  const int lane = threadIdx.x / COLS, d = threadIdx.x % COLS * 4;
+  const int64_t per = ONE ? p.q_heads : (p.q_heads + LANES - 1) / LANES;
+  const int64_t bt = blockIdx.x / (uint32_t)per;
+  const int head = (int)(blockIdx.x - bt * per) * (ONE ? 1 : LANES) + (ONE ? 0 : lane);
+  if (!ONE && (lane >= LANES || head >= p.q_heads)) return;
+  const int64_t row = bt * p.q_heads + head;
+  const First own = p.first[0][row];
+  if (own.more < 0) return;  // written whole
+  const int b = (int)(bt / p.q_tokens), t = (int)(bt - (int64_t)b * p.q_tokens);
+  const int kvh = head / p.per_head, in_seq = t * p.per_head + head - kvh * p.per_head;
+
+  float top = -INFINITY, total = 0.0f;
+  float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](float m, float l, const float* o) {
+    const float4v v = *(const float4v*)(o + d);
+    const float grown = m > top ? m : top;  // a NaN in l and O stays one in the sums
+    const float base = grown == -INFINITY ? 0.0f : grown;
+    const float keep = factor(top, base), f = factor(m, base);
+    total = total * keep + f * l;
+    acc = acc * keep + f * v;
+    top = grown;
+  };
+  // r: the row's number in its item's block
+  auto gather = [&](const First& first, const float* o, int r) {
+    if (!ONE || lane == 0) add(first.m, first.l, o);
+    for (int i = ONE ? lane : 0; i < first.more; i += ONE ? LANES : 1) {
+      const int64_t at = (int64_t)(first.next + i) * RB + r;
+      const float2 ml = p.next_ml[at];
+      add(ml.x, ml.y, p.next_o + at * D);
+    }
+  };
   if (p.groups > 0) {
     // the last group that starts at or before this row's sequence
-    const int b = (int)(row / ((int64_t)p.q_tokens * p.q_heads));
     int lo = 0, hi = p.groups;
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
@@ -584,20 +823,36 @@ __global__ __launch_bounds__(256) void attention_join(Params p) {
       else
         hi = mid;
     }
-    if (lo > 0 && b < p.group_offsets[lo]) first = 0;
+    if (lo > 0) {
+      const Members m = members_of(p, lo - 1);
+      if (b >= m.lo && b < m.hi && prefix_length(p, lo - 1) > 0)
+        gather(p.first[1][row], p.first_o[1] + row * D,
+               ((b - m.lo) * p.q_tokens * p.per_head + in_seq) % RB);
+    }
   }
-  const int parts = p.prefix_splits + p.own_splits;
-  float top = -INFINITY;
-  for (int i = first; i < parts; ++i) top = fmaxf(top, p.part_ml[(int64_t)i * p.rows + row].x);
+  gather(own, p.first_o[0] + row * D, in_seq % RB);
+  if constexpr (ONE) {
+    if (lane < LANES) {
+      acc_of[lane][d / 4] = acc;
+      if (d == 0) {
+        top_of[lane] = top;
+        total_of[lane] = total;
+      }
+    }
+    __syncthreads();
+    if (lane != 0) return;
+    for (int i = 1; i < LANES; ++i) top = top_of[i] > top ? top_of[i] : top;
+    const float base = top == -INFINITY ? 0.0f : top;
+    total = 0.0f;
+    acc = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < LANES; ++i) {
+      const float f = factor(top_of[i], base);
+      total += f * total_of[i];
+      acc += f * acc_of[i][d / 4];
+    }
+  }
   const float base = top == -INFINITY ? 0.0f : top;
-  float total = 0.0f;
-  float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int i = first; i < parts; ++i) {
-    const float2 ml = p.part_ml[(int64_t)i * p.rows + row];
-    const float f = factor(ml.x, base);
-    total += f * ml.y;
-    acc += f * *(const float4v*)(p.part_o + ((int64_t)i * p.rows + row) * D + d);
-  }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   *(uint2*)(p.out + row * D + d) = make_uint2(cvt_bf16x2(acc[0] * inv, acc[1] * inv),
                                               cvt_bf16x2(acc[2] * inv, acc[3] * inv));
@@ -609,17 +864,13 @@ __global__ __launch_bounds__(256) void attention_join(Params p) {
 
 struct Plan {
   int rt;  // 16-row tiles of queries per wavefront
-  int64_t own_blocks, own_splits, prefix_blocks, prefix_splits, rows;
-  bool direct;  // one part only: the first kernel writes the output
+  int64_t blocks, items, rows;
+  int64_t parts;   // 0: one workgroup per item
+  int64_t groups;  // workgroups
+  bool fits;       // every count within 31 bits
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
-
-// Workgroups to aim for: 256 CUs with two of 8 wavefronts each, twice over,
-// so that contexts of unequal length even out.
-constexpr int64_t kTargetGroups = 1024;
 
 Plan plan_of(int64_t page_size, int64_t kv_heads, int64_t head_dim, int64_t batch,
              int64_t q_tokens, int64_t q_heads, int64_t max_pages, int64_t max_prefix_pages,
@@ -627,38 +878,59 @@ Plan plan_of(int64_t page_size, int64_t kv_heads, int64_t head_dim, int64_t batc
   Plan p;
   const int64_t per_seq = q_tokens * (q_heads / kv_heads);
   p.rt = groups == 0 && per_seq <= 16 ? 1 : 2;
-  const int64_t rb = 16 * p.rt, waves = p.rt == 1 ? 8 : 4;
+  p.blocks = ceil_div(per_seq, 16 * p.rt);
   p.rows = batch * q_tokens * q_heads;
-  p.own_blocks = ceil_div(per_seq, rb);
-  p.prefix_blocks = groups ? batch * per_seq / rb + groups : 0;
-  // a part per workgroup: enough of them to fill the chip, each at least two rounds of its
-  // wavefronts' tiles long
-  const int64_t own_tokens = max_pages * page_size, prefix_tokens = max_prefix_pages * page_size;
-  p.own_splits = clamp64(ceil_div(kTargetGroups, batch * kv_heads * p.own_blocks), 1,
-                         clamp64(own_tokens / (2 * waves * kTile), 1, 64));
-  p.prefix_splits =
-      groups ? clamp64(ceil_div(kTargetGroups,
-                                clamp64(batch * per_seq / rb, 1, p.prefix_blocks) * kv_heads),
-                       1, clamp64(prefix_tokens / (2 * waves * kTile), 1, 64))
-             : 0;
-  p.direct = p.own_splits + p.prefix_splits == 1;
+  p.items = batch * p.blocks * kv_heads;
+  const int64_t held = 256 * groups_per_cu((int)head_dim, p.rt);
+  const int64_t tokens = max_pages * page_size;
+  // One workgroup per item where the contexts are short (a join costs about 5 us: 777 tokens
+  // 10.4 us so, 14.3 cut) or the items so many that their unequal lengths even out.  Else as
+  // many parts as the chip holds workgroups (with a prefix: 52 us so, 60 with twice as many),
+  // twice as many where an item is one sequence's (64 x 2048-8192 tokens: 98 us, 102 with one)
+  p.parts = groups == 0 && (tokens <= 2048 || p.items >= 8 * held) ? 0 : p.rt == 1 ? 2 * held : held;
+  // row blocks of all groups at most, and so parts at most: each cut adds one to an item's first
+  const int64_t prefix_items = groups ? (batch * per_seq / (16 * p.rt) + groups) * kv_heads : 0;
+  p.groups = p.items + (p.parts ? p.parts + prefix_items : 0);
+  const double tiles = (double)p.items * (double)ceil_div(tokens, kTile) +
+                       (double)prefix_items * (double)ceil_div(max_prefix_pages * page_size, kTile);
+  // the dispatch packet counts work-items in 32 bits
+  p.fits = p.groups <= ((int64_t)1 << 31) / 512 && p.rows <= ((int64_t)1 << 31) / 256 &&
+           (p.parts == 0 || tiles < 2147483648.0);
   return p;
+}
+
+int64_t first_parts(int64_t groups) { return groups ? 2 : 1; }
+
+template <int D, int RT>
+hipError_t join(const Params& p, const Plan& plan, hipStream_t stream) {
+  constexpr int64_t lanes = 256 / (D / 4);
+  // few rows: a workgroup for each, whose threads share its parts
+  if (plan.rows < 1024)
+    attention_join<D, RT, true><<<(uint32_t)plan.rows, 256, 0, stream>>>(p);
+  else
+    attention_join<D, RT, false><<<(uint32_t)(plan.rows / p.q_heads * ceil_div(p.q_heads, lanes)),
+                                   256, 0, stream>>>(p);
+  return hipGetLastError();
 }
 
 template <int D>
 hipError_t launch(const Params& p, const Plan& plan, hipStream_t stream) {
-  const int64_t grid = plan.prefix_blocks * p.kv_heads * plan.prefix_splits +
-                       (int64_t)p.batch * plan.own_blocks * p.kv_heads * plan.own_splits;
-  if (grid > ((int64_t)1 << 31) / 512) return hipErrorInvalidValue;
+  const uint32_t grid = (uint32_t)plan.groups;
+  if (plan.parts == 0) {
+    if (plan.rt == 1)
+      attention_items<D, 1, 8><<<grid, 512, 0, stream>>>(p);
+    else
+      attention_items<D, 2, 4><<<grid, 256, 0, stream>>>(p);
+    return hipGetLastError();
+  }
   if (plan.rt == 1)
-    attention_kernel<D, 1, 8><<<(uint32_t)grid, 512, 0, stream>>>(p);
+    attention_parts<D, 1><<<grid, 256, 0, stream>>>(p);
   else
-    attention_kernel<D, 2, 4><<<(uint32_t)grid, 256, 0, stream>>>(p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || plan.direct) return e;
-  const int64_t per = 256 / (D / 4);
-  attention_join<D><<<(uint32_t)ceil_div(plan.rows, per), 256, 0, stream>>>(p);
-  return hipGetLastError();
+    attention_parts<D, 2><<<grid, 256, 0, stream>>>(p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (plan.rt == 1) return join<D, 1>(p, plan, stream);
+  return join<D, 2>(p, plan, stream);
 }
 
 }  // namespace
@@ -669,12 +941,16 @@ int64_t kv_attention_workspace_bytes(int64_t page_size, int64_t kv_heads, int64_
                                      int64_t groups) {
   const Plan p = plan_of(page_size, kv_heads, head_dim, batch, q_tokens, q_heads, max_pages,
                          max_prefix_pages, groups);
-  return p.direct ? 0 : (p.own_splits + p.prefix_splits) * p.rows * (head_dim * 4 + 8);
+  return p.parts == 0
+             ? 0
+             : first_parts(groups) * p.rows * (head_dim * 4 + (int64_t)sizeof(First)) +
+                   p.parts * 16 * p.rt * (head_dim * 4 + 8);
 }
 
 hipError_t kv_attention_launch(const KvCache& c, const AttentionArgs& a, hipStream_t stream) {
   const Plan plan = plan_of(c.page_size, c.kv_heads, c.head_dim, a.batch, a.q_tokens, a.q_heads,
                             a.max_pages, a.max_prefix_pages, a.groups);
+  if (!plan.fits) return hipErrorInvalidValue;
   Params p;
   for (int i = 0; i < 2; ++i) {
     p.codes[i] = c.codes[i];
@@ -689,10 +965,17 @@ hipError_t kv_attention_launch(const KvCache& c, const AttentionArgs& a, hipStre
   p.group_offsets = a.group_offsets;
   p.out = (uint16_t*)a.out;
   p.lse = a.lse;
-  const int64_t parts = plan.own_splits + plan.prefix_splits;
-  p.part_o = plan.direct ? nullptr : (float*)a.workspace;
-  p.part_ml =
-      plan.direct ? nullptr : (float2*)((float*)a.workspace + parts * plan.rows * c.head_dim);
+  // sums, then the 16-byte and the 8-byte records
+  const int64_t parts = first_parts(a.groups), next = plan.parts * 16 * plan.rt;
+  float* o = (float*)a.workspace;
+  First* first = (First*)(o + (parts * plan.rows + next) * c.head_dim);
+  for (int i = 0; i < 2; ++i) {
+    const int64_t at = i < parts ? i * plan.rows : 0;
+    p.first_o[i] = o + at * c.head_dim;
+    p.first[i] = first + at;
+  }
+  p.next_o = o + parts * plan.rows * c.head_dim;
+  p.next_ml = (float2*)(first + parts * plan.rows);
   p.q_stride = a.q_stride;
   p.rows = plan.rows;
   p.num_pages = (int32_t)c.num_pages;
@@ -706,10 +989,8 @@ hipError_t kv_attention_launch(const KvCache& c, const AttentionArgs& a, hipStre
   p.max_pages = (int32_t)a.max_pages;
   p.max_prefix_pages = (int32_t)a.max_prefix_pages;
   p.groups = (int32_t)a.groups;
-  p.own_blocks = (int32_t)plan.own_blocks;
-  p.own_splits = (int32_t)plan.own_splits;
-  p.prefix_blocks = (int32_t)plan.prefix_blocks;
-  p.prefix_splits = (int32_t)plan.prefix_splits;
+  p.blocks = (int32_t)plan.blocks;
+  p.parts = (int32_t)plan.parts;
   p.scale = a.scale;
   switch (c.head_dim) {
     case 64: return launch<64>(p, plan, stream);

@@ -164,6 +164,27 @@ def test_long_contexts_in_many_parts():
     Batch(5, [100, 3], heads=4, kv_heads=2, dim=64, max_pages=600).check(label="wide table")
 
 
+@pytest.mark.parametrize("dim,heads,kv_heads,tokens", [(64, 4, 2, 1), (128, 8, 2, 1), (192, 6, 2, 2),
+                                                       (256, 2, 1, 1), (64, 20, 2, 3),
+                                                       (128, 40, 1, 1), (256, 9, 1, 3)])
+def test_wide_tables(dim, heads, kv_heads, tokens):
+    # tables with room for more than 2048 tokens: contexts laid end to end and cut into pieces,
+    # with cuts inside short and long ones, and empty ones between them
+    lens = [0, 700, 1, 64, 65, 0, 0, 1500, 63, 129, 2100, 5, 320]
+    Batch(dim + heads, lens, tokens=tokens, heads=heads, kv_heads=kv_heads, dim=dim, page=32,
+          max_pages=70).check(label="wide %d" % dim)
+
+
+def test_many_sequences():
+    # more sequences (and groups) than one round of a workgroup's threads
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 40, 300)
+    Batch(21, lens, heads=2, kv_heads=1, dim=64, max_pages=130).check(label="many")
+    members = np.minimum(np.arange(0, 291), 290)
+    Batch(22, lens, heads=2, kv_heads=1, dim=64, prefix_lens=rng.integers(0, 70, 290),
+          members=members).check(label="many groups")
+
+
 @pytest.mark.parametrize("gain,scale", [(1.0, 0.0), (1.0, -0.3), (30.0, 1.0), (2.0 ** 60, 2.0 ** -60),
                                         (2.0 ** -70, 2.0 ** 70), (1e-3, 1.0)])
 def test_scales_of_the_scores(gain, scale):
