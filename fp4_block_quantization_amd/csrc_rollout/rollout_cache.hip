@@ -8,21 +8,40 @@
 // one IEEE binary32 operation, in the definition's order, so the cache holds
 // the very bytes that nvfp4_quantize gives for the same rows.
 //
-// Both kernels only move data: one lane per 16-element block, a row's
-// blocks in neighbouring lanes, so a wavefront reads (or writes) 2 KiB of
-// consecutive BF16 and as many consecutive codes as the rows allow.
+// One lane per 16-element block, a row's blocks in neighbouring lanes: a
+// wavefront reads (or writes) 2 KiB of consecutive BF16, and whole rows of
+// codes.  Reading is bound by memory; writing about equally by the two
+// candidates' arithmetic, some 18 vector instructions an element.
 #include "fp4q_device.h"
 #include "rollout_launch.h"
 
 namespace fp4q {
 namespace {
 
+// Division of n < 2^31 by a divisor known on the host: a product and a
+// shift.  With l = ceil(log2 d) and m = ceil(2^(31+l) / d), m d = 2^(31+l) + r
+// with r < d, and n r < 2^(31+l) keeps the quotient exact.
+struct Divisor {
+  uint32_t d, m, shift;
+};
+
+Divisor divisor_of(uint32_t d) {
+  uint32_t l = 0;
+  while (((uint64_t)1 << l) < d) ++l;
+  return {d, (uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d), 31 + l};
+}
+
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor& v) {
+  return (uint32_t)(((uint64_t)n * v.m) >> v.shift);
+}
+
 struct CacheView {
   uint8_t* codes[2];
   uint8_t* scales[2];
   float* token_scales[2];
   int64_t slots;  // num_pages * page_size
-  int32_t page_size, heads, blocks;  // blocks: head_dim / 16
+  Divisor page_size, heads;
+  int32_t blocks;  // head_dim / 16
 };
 
 CacheView view_of(const KvCache& c) {
@@ -33,55 +52,75 @@ CacheView view_of(const KvCache& c) {
     v.token_scales[i] = c.token_scales[i];
   }
   v.slots = c.num_pages * c.page_size;
-  v.page_size = (int32_t)c.page_size;
-  v.heads = (int32_t)c.kv_heads;
+  v.page_size = divisor_of((uint32_t)c.page_size);
+  v.heads = divisor_of((uint32_t)c.kv_heads);
   v.blocks = (int32_t)(c.head_dim / 16);
   return v;
 }
 
 struct Place {
-  int64_t row;       // index of the cache row: codes at row * d/2, scale at row
-  int64_t key_byte;  // of this lane's block scale in k_scales
-  int64_t val_byte;  // and in v_scales
+  int64_t row;    // index of the cache row: codes at row * d/2, scale at row
+  int64_t scale;  // of this lane's block among the block scales
 };
 
-__device__ __forceinline__ Place place_of(const CacheView& c, uint32_t slot, int head, int block) {
-  const uint32_t page = slot / (uint32_t)c.page_size, at = slot - page * (uint32_t)c.page_size;
-  const int64_t ph = (int64_t)page * c.heads + head;
+__device__ __forceinline__ Place place_of(const CacheView& c, uint32_t slot, uint32_t head,
+                                          int block, int which) {
+  const uint32_t page = quotient(slot, c.page_size), at = slot - page * c.page_size.d;
+  const int64_t ph = (int64_t)page * c.heads.d + head;
   Place p;
-  p.row = ph * c.page_size + at;
-  p.key_byte = p.row * c.blocks + block;
-  p.val_byte = (ph * c.blocks + block) * c.page_size + at;
+  p.row = ph * c.page_size.d + at;
+  p.scale = which ? (ph * c.blocks + block) * c.page_size.d + at : p.row * c.blocks + block;
   return p;
 }
 
 // One candidate of a block: its scale byte, codes and squared error.
 struct Candidate {
-  uint32_t e_byte, lo, hi;
+  uint32_t e_byte;
+  uint32_t word[2];
   float err;
 };
 
 __device__ __forceinline__ Candidate candidate(const float* x, float b, float s, float k) {
   Candidate c;
-  float e;
-  c.e_byte = e4m3_encode(b / (k * s), e);
-  const float d = e * s;
-  const float r = d > 0.0f ? 1.0f / d : 0.0f;
-  uint32_t w[2] = {0u, 0u};
-  float err = 0.0f;
+  // a zero row (s = 0) has zero scales; the quotient rounds to at most 448
+  const float t = s > 0.0f ? fminf(b / (k * s), 448.0f) : 0.0f;
+  c.e_byte = cvt_e4m3x2(t, t) & 0xFFu;
+  const float e = e4m3_value<0>(c.e_byte), d = e * s;
+  c.err = 0.0f;
+  if (d >= 0x1p-126f || d == 0.0f) {
+    // d = 0: every code is a zero with the element's sign
+    const float r = d == 0.0f ? 0.0f : recip_normal(d);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const float* v = x + 8 * w;
+      uint32_t q = cvt_e2m1x2<0>(any_word(), v[0] * r, v[1] * r);
+      q = cvt_e2m1x2<1>(q, v[2] * r, v[3] * r);
+      q = cvt_e2m1x2<2>(q, v[4] * r, v[5] * r);
+      q = cvt_e2m1x2<3>(q, v[6] * r, v[7] * r);
+      c.word[w] = q;
+      const float2v g[4] = {e2m1x2_values<0>(q), e2m1x2_values<1>(q), e2m1x2_values<2>(q),
+                            e2m1x2_values<3>(q)};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float diff = v[i] - (g[i / 2][i % 2] * e) * s;
+        c.err = c.err + diff * diff;
+      }
+    }
+    return c;
+  }
+  // a subnormal step, whose reciprocal may be infinite: the conversions' domain ends here
+  const float r = 1.0f / d;
+  c.word[0] = c.word[1] = 0u;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float g;
     const uint32_t code = e2m1_code_sw(__builtin_fabsf(x[i]) * r, g);
     const uint32_t sign = __float_as_uint(x[i]) >> 31;
-    w[i >> 3] |= (code | sign << 3) << (4 * (i & 7));
+    c.word[i >> 3] |= (code | sign << 3) << (4 * (i & 7));
     const float v = (g * e) * s;
     const float diff = x[i] - (sign ? -v : v);
-    err = err + diff * diff;
+    c.err = c.err + diff * diff;
   }
-  c.lo = w[0];
-  c.hi = w[1];
-  c.err = err;
   return c;
 }
 
@@ -90,15 +129,14 @@ __device__ __forceinline__ Candidate candidate(const float* x, float b, float s,
 template <int LANES>
 __global__ __launch_bounds__(256) void kv_append_kernel(CacheView c, const uint16_t* k,
                                                         int64_t k_stride, const uint16_t* v,
-                                                        int64_t v_stride, int64_t tokens,
+                                                        int64_t v_stride, uint32_t rows,
                                                         const int64_t* slots, int fos) {
   const int which = blockIdx.y;
-  const int64_t unit = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  const uint32_t row = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   const int block = threadIdx.x % LANES;
-  const int64_t token = unit / c.heads;
-  const int head = (int)(unit - token * c.heads);
-  const bool live = token < tokens && block < c.blocks;
-  const int64_t slot = token < tokens ? slots[token] : -1;
+  const uint32_t token = quotient(row, c.heads), head = row - token * c.heads.d;
+  const bool live = row < rows && block < c.blocks;
+  const int64_t slot = row < rows ? slots[token] : -1;
   float x[16];
   float b = 0.0f;
 #pragma unroll
@@ -106,65 +144,63 @@ __global__ __launch_bounds__(256) void kv_append_kernel(CacheView c, const uint1
   if (live) {
     const uint16_t* src = (which ? v + token * v_stride : k + token * k_stride) +
                           (int64_t)head * c.blocks * 16 + block * 16;
-    const uint4 a = ((const uint4*)src)[0], z = ((const uint4*)src)[1];
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, z.x, z.y, z.z, z.w};
+    const u32x4v a = ((const u32x4v*)src)[0], z = ((const u32x4v*)src)[1];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      x[2 * i] = bf16_lo(w[i]);
-      x[2 * i + 1] = bf16_hi(w[i]);
+      const uint32_t w = i < 4 ? a[i] : z[i - 4];
+      x[2 * i] = bf16_lo(w);
+      x[2 * i + 1] = bf16_hi(w);
       b = fmaxf(b, fmaxf(__builtin_fabsf(x[2 * i]), __builtin_fabsf(x[2 * i + 1])));
     }
   }
   float amax = b;
 #pragma unroll
   for (int step = LANES / 2; step > 0; step >>= 1) amax = fmaxf(amax, __shfl_xor(amax, step));
-  const float s = amax / (fos ? 1536.0f : 2688.0f);
+  const float s = amax_over_c(amax, fos != 0);
   Candidate q = candidate(x, b, s, 6.0f);
   if (fos) {
     const Candidate q4 = candidate(x, b, s, 4.0f);
     if (q4.err < q.err) q = q4;
   }
   if (!live || slot < 0 || slot >= c.slots) return;
-  const Place p = place_of(c, (uint32_t)slot, head, block);
-  ((uint2*)c.codes[which])[p.row * c.blocks + block] = make_uint2(q.lo, q.hi);
-  c.scales[which][which ? p.val_byte : p.key_byte] = (uint8_t)q.e_byte;
+  const Place p = place_of(c, (uint32_t)slot, head, block, which);
+  ((u32x2v*)c.codes[which])[p.row * c.blocks + block] = (u32x2v){q.word[0], q.word[1]};
+  c.scales[which][p.scale] = (uint8_t)q.e_byte;
   if (block == 0) c.token_scales[which][p.row] = s;
 }
 
-__global__ __launch_bounds__(256) void kv_read_kernel(CacheView c, const int64_t* slots,
-                                                      int64_t tokens, uint4* k_out,
-                                                      uint4* v_out) {
+__global__ __launch_bounds__(256) void kv_read_kernel(CacheView c, Divisor blocks,
+                                                      const int64_t* slots, uint32_t units,
+                                                      u32x4v* k_out, u32x4v* v_out) {
   const int which = blockIdx.y;
-  const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;  // a 16-element block
-  const int64_t row = unit / c.blocks;
-  const int block = (int)(unit - row * c.blocks);
-  const int64_t token = row / c.heads;
-  if (token >= tokens) return;
-  const int head = (int)(row - token * c.heads);
+  const uint32_t unit = blockIdx.x * 256 + threadIdx.x;  // a 16-element block
+  if (unit >= units) return;
+  const uint32_t row = quotient(unit, blocks), token = quotient(row, c.heads);
+  const int block = (int)(unit - row * blocks.d);
   const int64_t slot = slots[token];
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = 0u;
+  u32x4v w[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
   if (slot >= 0 && slot < c.slots) {
-    const Place p = place_of(c, (uint32_t)slot, head, block);
-    const uint2 q = ((const uint2*)c.codes[which])[p.row * c.blocks + block];
-    const float e = e4m3_decode(c.scales[which][which ? p.val_byte : p.key_byte]);
+    const Place p = place_of(c, (uint32_t)slot, row - token * c.heads.d, block, which);
+    const u32x2v q = ((const u32x2v*)c.codes[which])[p.row * c.blocks + block];
+    const float e = e4m3_value<0>(c.scales[which][p.scale]);
     const float s = c.token_scales[which][p.row];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t byte = (i < 4 ? q.x : q.y) >> (8 * (i & 3));
-      const float a = (e2m1_value(byte & 7u) * e) * s, z = (e2m1_value(byte >> 4 & 7u) * e) * s;
-      w[i] = cvt_bf16x2((byte & 8u) ? -a : a, (byte & 0x80u) ? -z : z);
+    for (int h = 0; h < 2; ++h) {
+      const float2v g[4] = {e2m1x2_values<0>(q[h]), e2m1x2_values<1>(q[h]),
+                            e2m1x2_values<2>(q[h]), e2m1x2_values<3>(q[h])};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[h][i] = cvt_bf16x2((g[i][0] * e) * s, (g[i][1] * e) * s);
     }
   }
-  uint4* out = (which ? v_out : k_out) + unit * 2;
-  out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  u32x4v* out = (which ? v_out : k_out) + (int64_t)unit * 2;
+  out[0] = w[0];
+  out[1] = w[1];
 }
 
 }  // namespace
 
-// The dispatch packet counts work-items in 32 bits: longer calls go in several
+// Work-items of a launch are counted in 31 bits: longer calls go in several
 // launches over consecutive tokens.
 static int64_t tokens_per_launch(int64_t lanes_per_token) {
   const int64_t n = ((int64_t)1 << 30) / lanes_per_token;
@@ -179,14 +215,14 @@ hipError_t kv_append_launch(const KvCache& cache, const void* k, int64_t k_strid
   while (lanes < c.blocks) lanes *= 2;
   const int64_t per = 256 / lanes, step = tokens_per_launch(lanes * cache.kv_heads);
   for (int64_t t0 = 0; t0 < tokens; t0 += step) {
-    const int64_t n = tokens - t0 < step ? tokens - t0 : step;
-    const dim3 g((uint32_t)((n * c.heads + per - 1) / per), 2);
+    const int64_t n = tokens - t0 < step ? tokens - t0 : step, rows = n * cache.kv_heads;
+    const dim3 g((uint32_t)((rows + per - 1) / per), 2);
     const uint16_t* kt = (const uint16_t*)k + t0 * k_stride;
     const uint16_t* vt = (const uint16_t*)v + t0 * v_stride;
-#define FP4Q_APPEND(L)                                                                       \
-  case L:                                                                                    \
-    kv_append_kernel<L><<<g, 256, 0, stream>>>(c, kt, k_stride, vt, v_stride, n, slots + t0, \
-                                               four_over_six);                               \
+#define FP4Q_APPEND(L)                                                                     \
+  case L:                                                                                  \
+    kv_append_kernel<L><<<g, 256, 0, stream>>>(c, kt, k_stride, vt, v_stride,              \
+                                               (uint32_t)rows, slots + t0, four_over_six); \
     break;
     switch (lanes) {
       FP4Q_APPEND(1)
@@ -206,12 +242,13 @@ hipError_t kv_append_launch(const KvCache& cache, const void* k, int64_t k_strid
 hipError_t kv_read_launch(const KvCache& cache, const int64_t* slots, int64_t tokens, void* k_out,
                           void* v_out, hipStream_t stream) {
   const CacheView c = view_of(cache);
-  const int64_t per_token = (int64_t)c.heads * c.blocks, step = tokens_per_launch(per_token);
+  const int64_t per_token = cache.kv_heads * c.blocks, step = tokens_per_launch(per_token);
   for (int64_t t0 = 0; t0 < tokens; t0 += step) {
-    const int64_t n = tokens - t0 < step ? tokens - t0 : step;
-    const dim3 g((uint32_t)((n * per_token + 255) / 256), 2);
-    kv_read_kernel<<<g, 256, 0, stream>>>(c, slots + t0, n, (uint4*)k_out + t0 * per_token * 2,
-                                          (uint4*)v_out + t0 * per_token * 2);
+    const int64_t units = (tokens - t0 < step ? tokens - t0 : step) * per_token;
+    const dim3 g((uint32_t)((units + 255) / 256), 2);
+    kv_read_kernel<<<g, 256, 0, stream>>>(c, divisor_of((uint32_t)c.blocks), slots + t0,
+                                          (uint32_t)units, (u32x4v*)k_out + t0 * per_token * 2,
+                                          (u32x4v*)v_out + t0 * per_token * 2);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -4,28 +4,30 @@
 // Both forms read every weight byte once per 16 * RT (or ROWS) rows of x
 // and are bound by that read: 0.5625 bytes a weight (NVFP4), 0.53 (MXFP4).
 //
-// Few rows (dot form).  A wavefront takes NC output columns; a lane takes 32
-// consecutive weights of a column at a time (16 bytes of codes, so a load
-// covers 1 KiB of a column) and multiplies them with BF16 dot products:
+// One or two rows (dot form).  A wavefront takes NC output columns; a lane
+// takes 32 consecutive weights of a column at a time (16 bytes of codes, so a
+// load covers 1 KiB of a column) and multiplies them with BF16 dot products:
 //   y = s sum_b e_b (sum_{i in b} g_i x_i), the inner sum over raw codes,
 // so a scale costs one FMA per 16 weights and row.
 //
 // More rows (matrix form).  Weights are the rows of a 16x16x32 matrix
-// instruction, activations its columns.  An NVFP4 weight enters as g e, an
-// exact FP16 number (one conversion and one packed product per two weights),
-// the activations as FP16 scaled by a power of two per row (exact for
-// elements within 2^29 of the row's largest), converted by a small kernel
-// before; an MXFP4 weight is an exact BF16 number that the conversion's own
-// scale operand gives, and the activations stay as they are.  Slabs of the
-// activations are copied to LDS, once for the workgroup's four wavefronts,
-// and the weights to registers, one slab ahead of their use.
+// instruction, activations its columns.  A weight enters as an exact BF16
+// number: g e of NVFP4 has at most 6 significant bits, g 2^E of MXFP4 at
+// most 2 (the conversion's own scale operand gives it), and the activations
+// enter as they are.  Widening to FP16 instead takes half the vector
+// instructions an NVFP4 weight (packed products), but then the activations
+// have to be brought into FP16's range by a kernel before, which costs more
+// than it gives.  Large matrices: slabs of the activations are copied to
+// LDS, once for the workgroup's four wavefronts, and the weights to
+// registers, one slab ahead of their use.  Small ones: the wavefronts of a
+// workgroup share 16 columns and divide k, so that even a few columns make
+// enough wavefronts without a second kernel to join them.
 #include "fp4q_device.h"
 #include "rollout_launch.h"
 
 namespace fp4q {
 namespace {
 
-typedef _Float16 half8v __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
 typedef short short2v __attribute__((ext_vector_type(2)));
 typedef float float4v __attribute__((ext_vector_type(4)));
@@ -47,13 +49,6 @@ __device__ __forceinline__ void put_out(const LinearArgs& a, int64_t at, float v
     ((__bf16*)a.out)[at] = (__bf16)v;
 }
 
-// The two E4M3 bytes of a word's low (0) or high (1) half as FP16, exact.
-template <int SEL>
-__device__ __forceinline__ half2v e4m3_f16x2(uint32_t w) {
-  return __builtin_bit_cast(half2v,
-                            __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, SEL != 0));
-}
-
 template <int SEL>
 __device__ __forceinline__ bf16x2v e2m1_bf16x2(uint32_t w, float scale) {
   return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, SEL);
@@ -64,7 +59,7 @@ __device__ __forceinline__ float dot2(bf16x2v a, uint32_t b, float c) {
                                          __builtin_bit_cast(short2v, b), c, false);
 }
 
-// ---- few rows -----------------------------------------------------------------
+// ---- one or two rows -----------------------------------------------------------------
 
 // WAVES wavefronts of NC columns each share the activations in LDS, a chunk
 // of KC elements of k at a time: read from global memory by the lanes that
@@ -193,38 +188,102 @@ __global__ __launch_bounds__(64 * WAVES) void linear_dot(LinearArgs a, int64_t x
 
 // ---- more rows ----------------------------------------------------------------
 
-// Rows of x as FP16 times a power of two that takes the row's largest
-// element to [2^14, 2^15), and the power's inverse.  Zeros, and rows with a
-// NaN or infinity, stay as they are.
-__global__ __launch_bounds__(256) void linear_convert(LinearArgs a, int64_t row0, uint16_t* to,
-                                                      float* scale) {
-  __shared__ uint32_t tops[4];
-  const int64_t row = row0 + blockIdx.x, pieces = a.k / 8;
-  const u32x4v* x = (const u32x4v*)((const uint16_t*)a.x + row * a.k);
-  uint32_t top = 0;
-  for (int64_t i = threadIdx.x; i < pieces; i += 256) {
-    const u32x4v v = x[i];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7FFFu, v[j] >> 16 & 0x7FFFu));
+// Eight weights of a word of codes as BF16, exact.  f: MXFP4's power of two,
+// or NVFP4's block scale.
+template <bool MX>
+__device__ __forceinline__ bf16x8v weights_of(uint32_t word, float f) {
+  if constexpr (MX) {
+    const bf16x2v a = e2m1_bf16x2<0>(word, f), b = e2m1_bf16x2<1>(word, f);
+    const bf16x2v c = e2m1_bf16x2<2>(word, f), d = e2m1_bf16x2<3>(word, f);
+    return (bf16x8v){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+  } else {
+    const float2v a = e2m1x2_values<0>(word), b = e2m1x2_values<1>(word);
+    const float2v c = e2m1x2_values<2>(word), d = e2m1x2_values<3>(word);
+    const u32x4v w = {cvt_bf16x2(a[0] * f, a[1] * f), cvt_bf16x2(b[0] * f, b[1] * f),
+                      cvt_bf16x2(c[0] * f, c[1] * f), cvt_bf16x2(d[0] * f, d[1] * f)};
+    return __builtin_bit_cast(bf16x8v, w);
   }
+}
+
+__device__ __forceinline__ float4v product(bf16x8v w, u32x4v x, float4v acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8v, x), acc, 0, 0, 0);
+}
+
+// Small matrices.  Wavefront w of WAVES takes the steps of 128 elements of k
+// w, w + WAVES, ... for 16 columns and up to 16 * RT rows; activations come
+// straight from global memory (the cache serves the workgroups' repeats).
+template <bool MX, int RT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void linear_small(LinearArgs a) {
+  constexpr int RB = 16 * RT;
+  __shared__ float sums[WAVES][RB][17];
+  const int lane = threadIdx.x % 64, col = lane % 16, grp = lane / 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t k = a.k, n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * RB;
+  const int64_t n = min(n0 + col, a.n - 1), steps = (k + 127) / 128;
+  const uint8_t* codes = a.codes + n * (k / 2) + grp * 16;
+  const uint8_t* scales = a.scales + n * (k / (MX ? 32 : 16)) + grp * (MX ? 1 : 2);
+  const uint16_t* x[RT];
 #pragma unroll
-  for (int s = 32; s > 0; s >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, s));
-  if (threadIdx.x % 64 == 0) tops[threadIdx.x / 64] = top;
-  __syncthreads();
-  top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-  const int field = (int)(top >> 7);
-  const int ex = top == 0 || field == 255 ? 0 : 14 + 127 - max(field, 1);
-  for (int64_t i = threadIdx.x; i < pieces; i += 256) {
-    u32x4v v = x[i];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const half2v h = {(_Float16)__builtin_ldexpf(bf16_lo(v[j]), ex),
-                        (_Float16)__builtin_ldexpf(bf16_hi(v[j]), ex)};
-      v[j] = __builtin_bit_cast(uint32_t, h);
+  for (int r = 0; r < RT; ++r)
+    x[r] = (const uint16_t*)a.x + min(m0 + r * 16 + col, a.rows - 1) * k;
+
+  struct Step {
+    u32x4v w, x[RT][4];
+    uint32_t e;
+  };
+  auto load = [&](int64_t step, Step& s) {
+    const int64_t k0 = step * 128 + grp * 32;
+    s.w = (u32x4v){0, 0, 0, 0};
+    s.e = 0;
+    if (k0 + 32 <= k) {
+      s.w = *(const u32x4v*)(codes + step * 64);
+      if constexpr (MX)
+        s.e = scales[step * 4];
+      else
+        s.e = *(const uint16_t*)(scales + step * 8);
+    } else if (!MX && k0 + 16 <= k) {
+      const u32x2v half = *(const u32x2v*)(codes + step * 64);
+      s.w = (u32x4v){half[0], half[1], 0, 0};
+      s.e = scales[step * 8];
     }
-    ((u32x4v*)(to + row * a.k))[i] = v;
+    // pieces past k repeat the row's last one, times weights 0
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        s.x[r][q] = *(const u32x4v*)(x[r] + min(k0 + q * 8, k - 8));
+  };
+  float4v acc[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) acc[r] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
+  Step next;
+  if (wave < steps) load(wave, next);
+  for (int64_t step = wave; step < steps; step += WAVES) {
+    const Step now = next;
+    if (step + WAVES < steps) load(step + WAVES, next);
+    const float f0 = MX ? __uint_as_float(now.e << 23) : e4m3_value<0>(now.e);
+    const float f1 = MX ? f0 : e4m3_value<1>(now.e);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bf16x8v w = weights_of<MX>(now.w[q], q < 2 ? f0 : f1);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[r] = product(w, now.x[r][q], acc[r]);
+    }
   }
-  if (threadIdx.x == 0) scale[row] = __builtin_ldexpf(1.0f, -ex);
+  // lane (col, grp) holds columns n0 + 4 grp + i of row m0 + 16 r + col
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[wave][r * 16 + col][grp * 4 + i] = acc[r][i];
+  __syncthreads();
+  for (int at = threadIdx.x; at < RB * 16; at += 64 * WAVES) {
+    const int64_t m = m0 + at / 16, to = n0 + at % 16;
+    if (m >= a.rows || to >= a.n) continue;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) sum += sums[w][at / 16][at % 16];
+    put_out(a, m * a.n + to, MX ? sum : sum * a.row_scales[to]);
+  }
 }
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -258,55 +317,64 @@ struct ScaleLoad {
     for (int i = 0; i < BYTES; ++i)
       if (i < n) w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
   }
-  // NVFP4: the two bytes of step s in the low (s < 2) or high half of e[s % 2]; MXFP4: in
-  // e[s] the FP32 pattern of step s's power of two (the conversions read the exponent field
-  // alone, so byte 0, 2^-127, works too).
-  __device__ __forceinline__ void exchange(int col, int grp, uint32_t (&e)[STEPS]) const {
+  // f[s][h]: the scale of the lane's first (0) and second (1) 16 elements of step s; MXFP4's
+  // power of two, an FP32 pattern of which the conversions read the exponent field alone (so
+  // byte 0, 2^-127, works too), in f[s][0].
+  __device__ __forceinline__ void exchange(int col, int grp, float (&f)[STEPS][2]) const {
     if constexpr (BYTES == 8) {
       // lane group g holds, of step g, the pairs for groups 0 ... 3; a 4 x 4 transposition
       const auto h = __builtin_amdgcn_permlane32_swap(w[0], w[1], false, false);
       const uint32_t lo = __builtin_amdgcn_perm(h[1], h[0], 0x05040100u);
       const uint32_t hi = __builtin_amdgcn_perm(h[1], h[0], 0x07060302u);
       const auto r = __builtin_amdgcn_permlane16_swap(lo, hi, false, false);
-      e[0] = r[0], e[1] = r[1];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {  // r[s]: the pairs of steps s and s + 2
+        f[s][0] = e4m3_value<0>(r[s]);
+        f[s][1] = e4m3_value<1>(r[s]);
+        f[s + 2][0] = e4m3_value<2>(r[s]);
+        f[s + 2][1] = e4m3_value<3>(r[s]);
+      }
     } else if constexpr (!MX) {
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-        e[s] = (uint32_t)__shfl((int)w[0], col + 16 * (2 * s + grp / 2)) >> (16 * (grp % 2));
-    } else if constexpr (BYTES == 4) {
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-        e[s] = ((uint32_t)__shfl((int)w[0], col + 16 * s) >> (8 * grp) & 255u) << 23;
+      for (int s = 0; s < STEPS; ++s) {
+        const uint32_t e =
+            (uint32_t)__shfl((int)w[0], col + 16 * (2 * s + grp / 2)) >> (16 * (grp % 2));
+        f[s][0] = e4m3_value<0>(e);
+        f[s][1] = e4m3_value<1>(e);
+      }
     } else {
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-        e[s] = ((uint32_t)__shfl((int)w[0], col + 16 * (2 * s + grp / 2)) >> (8 * (grp % 2)) &
-                255u)
-               << 23;
+      for (int s = 0; s < STEPS; ++s) {
+        const int from = BYTES == 4 ? s : 2 * s + grp / 2, byte = BYTES == 4 ? grp : grp % 2;
+        const uint32_t e = (uint32_t)__shfl((int)w[0], col + 16 * from) >> (8 * byte) & 255u;
+        f[s][0] = __uint_as_float(e << 23);
+      }
     }
   }
 };
 
 // One workgroup: 64 * NT columns (tile x0 + blockIdx.x), 16 * RT rows (block
-// y0 + blockIdx.y; with groups, all rows of that group in turn), split
-// blockIdx.z of the slabs of KS elements of k.  x: the activations as the
-// matrix instruction takes them, x_scale: NVFP4's inverse row scales.
+// y0 + blockIdx.y; with groups, all rows of that group in turn), and the
+// blockIdx.z-th share of k's slabs of KS elements; with several shares the
+// sums go to `partial`.
 template <bool MX, int RT, int NT>
-__global__ __launch_bounds__(256) void linear_mfma(LinearArgs a, const uint16_t* x,
-                                                   const float* x_scale, int64_t x0, int64_t y0,
-                                                   int splits, float* partial) {
+__global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs a, int64_t x0,
+                                                                     int64_t y0, float* partial) {
   constexpr int KS = RT == 1 ? 512 : 256, STEPS = KS / 128, RB = 16 * RT;
   constexpr int PIECES = KS / 8, PER_COPY = 64 / PIECES;  // 16-byte pieces a row; rows a copy
   __shared__ alignas(16) uint8_t xs[2][RB * KS * 2];
   const int lane = threadIdx.x % 64, col = lane % 16, grp = lane / 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int64_t k = a.k, y = y0 + blockIdx.y;
-  const int split = blockIdx.z;
+  const uint16_t* x = (const uint16_t*)a.x;
+  const int64_t splits = gridDim.z, split = blockIdx.z;
   const Range range = a.offsets ? rows_of(a, y) : Range{y * RB, a.rows};
   const int64_t matrix = a.offsets ? y : 0;
-  const int64_t slabs = (k + KS - 1) / KS;
-  const int64_t slab_lo = slabs * split / splits, slab_hi = slabs * (split + 1) / splits;
-  const int64_t n0 = (x0 + blockIdx.x) * 64 * NT + wave * 16 * NT;
+  // whole slabs [slab_lo, slab_whole), and after them perhaps k's last part
+  const int slabs = (int)((k + KS - 1) / KS);
+  const int slab_lo = (int)(slabs * split / splits), slab_hi = (int)(slabs * (split + 1) / splits);
+  const int slab_whole = min(slab_hi, (int)(k / KS));
+  const int64_t n0 = ((x0 + blockIdx.x) * 4 + wave) * 16 * NT;
   const uint8_t* codes[NT];
   const uint8_t* scales[NT];
 #pragma unroll
@@ -325,65 +393,40 @@ __global__ __launch_bounds__(256) void linear_mfma(LinearArgs a, const uint16_t*
     const int rows = (int)min((int64_t)RB, range.last - m0);
     u32x4v w[NT][STEPS], w_next[NT][STEPS];
     ScaleLoad<MX, KS> e_next[NT];
-    uint32_t e[NT][STEPS];
-    auto load = [&](int64_t slab, u32x4v (&wv)[NT][STEPS], ScaleLoad<MX, KS> (&ev)[NT]) {
-      const int64_t k0 = slab * KS;
-      // activations: a copy fills 64 pieces; rows past the last are left as they are (their
-      // columns of the result are not stored), pieces past k repeat the last (times weights 0)
-#pragma unroll
-      for (int i = 0; i < RB / PER_COPY / 4; ++i) {
-        const int first = (i * 4 + wave) * PER_COPY;
-        if (first < rows) {
-          const int r = first + lane / PIECES;
-          const int64_t piece = min(k0 / 8 + ((lane % PIECES) ^ (r & 15)), k / 8 - 1);
-          __builtin_amdgcn_global_load_lds(
-              x + (m0 + min(r, rows - 1)) * k + piece * 8,
-              (lds_void*)(xs[slab & 1] + first * KS * 2), 16, 0, 0);
-        }
-      }
-      const int left = (int)min((int64_t)KS, k - k0);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint8_t* c = codes[t] + k0 / 2;
-        const uint8_t* b = scales[t] + k0 / (MX ? 32 : 16);
-        if (left == KS) {
-#pragma unroll
-          for (int s = 0; s < STEPS; ++s) wv[t][s] = *(const u32x4v*)(c + s * 64);
-          ev[t].whole(b);
-        } else {
-#pragma unroll
-          for (int s = 0; s < STEPS; ++s) {
-            const int at = s * 128 + grp * 32;
-            wv[t][s] = (u32x4v){0, 0, 0, 0};
-            if (at + 32 <= left) {
-              wv[t][s] = *(const u32x4v*)(c + s * 64);
-            } else if (!MX && at + 16 <= left) {
-              const u32x2v half = *(const u32x2v*)(c + s * 64);
-              wv[t][s] = (u32x4v){half[0], half[1], 0, 0};
-            }
-          }
-          ev[t].some(b, left / (MX ? 32 : 16) - grp * ScaleLoad<MX, KS>::BYTES);
-        }
-      }
-    };
     float4v acc[NT][RT];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[t][r] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
 
-    if (m0 != range.first) __syncthreads();  // the last rows' slabs are read
-    if (slab_lo < slab_hi) load(slab_lo, w_next, e_next);
-    for (int64_t slab = slab_lo; slab < slab_hi; ++slab) {
+    // a slab's activations: a copy fills 64 pieces; rows past the last are left as they are
+    // (their columns of the result are not stored), pieces past k repeat the last one (times
+    // weights 0)
+    auto copy = [&](int slab) {
+      const int64_t piece0 = (int64_t)slab * PIECES, last = k / 8 - 1;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int i = 0; i < RB / PER_COPY / 4; ++i) {
+        const int first = (i * 4 + wave) * PER_COPY;
+        if (first < rows) {
+          const int r = first + lane / PIECES;
+          const int64_t piece = min(piece0 + ((lane % PIECES) ^ (r & 15)), last);
+          __builtin_amdgcn_global_load_lds(x + (m0 + min(r, rows - 1)) * k + piece * 8,
+                                           (lds_void*)(xs[slab & 1] + first * KS * 2), 16, 0, 0);
+        }
+      }
+    };
+    auto load = [&](int slab) {
+      copy(slab);
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) w[t][s] = w_next[t][s];
-      __builtin_amdgcn_s_waitcnt(0);  // this wavefront's copies of the slab have landed
+      for (int t = 0; t < NT; ++t) {
+        const uint8_t* c = codes[t] + (int64_t)slab * (KS / 2);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) e_next[t].exchange(col, grp, e[t]);
-      __syncthreads();                // and the others'; the slab before is read
-      if (slab + 1 < slab_hi) load(slab + 1, w_next, e_next);
+        for (int s = 0; s < STEPS; ++s) w_next[t][s] = *(const u32x4v*)(c + s * 64);
+        e_next[t].whole(scales[t] + (int64_t)slab * (KS / (MX ? 32 : 16)));
+      }
+    };
+    // the slab of w, whose scales are in e_next
+    auto multiply = [&](int slab, float (&f)[NT][STEPS][2]) {
       const uint8_t* xb = xs[slab & 1];
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
@@ -396,35 +439,56 @@ __global__ __launch_bounds__(256) void linear_mfma(LinearArgs a, const uint16_t*
               xv[r] = *(const u32x4v*)(xb + at_piece[q] + r * 16 * KS * 2 + s * 256);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const uint32_t word = w[t][s][q];
-            if constexpr (MX) {
-              const float sc = __uint_as_float(e[t][s]);
-              const bf16x2v b0 = e2m1_bf16x2<0>(word, sc), b1 = e2m1_bf16x2<1>(word, sc);
-              const bf16x2v b2 = e2m1_bf16x2<2>(word, sc), b3 = e2m1_bf16x2<3>(word, sc);
-              const bf16x8v wv = {b0[0], b0[1], b1[0], b1[1], b2[0], b2[1], b3[0], b3[1]};
+            const bf16x8v wv = weights_of<MX>(w[t][s][q], f[t][s][MX ? 0 : q / 2]);
 #pragma unroll
-              for (int r = 0; r < RT; ++r)
-                if (r == 0 || r * 16 < rows)
-                  acc[t][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                      wv, __builtin_bit_cast(bf16x8v, xv[r]), acc[t][r], 0, 0, 0);
-            } else {
-              const half2v both =
-                  STEPS == 4 && s >= 2 ? e4m3_f16x2<1>(e[t][s % 2]) : e4m3_f16x2<0>(e[t][s % 2]);
-              const half2v sc = {both[q / 2], both[q / 2]};
-              const half2v h0 = e2m1x2_values_f16<0>(word) * sc;
-              const half2v h1 = e2m1x2_values_f16<1>(word) * sc;
-              const half2v h2 = e2m1x2_values_f16<2>(word) * sc;
-              const half2v h3 = e2m1x2_values_f16<3>(word) * sc;
-              const half8v wv = {h0[0], h0[1], h1[0], h1[1], h2[0], h2[1], h3[0], h3[1]};
-#pragma unroll
-              for (int r = 0; r < RT; ++r)
-                if (r == 0 || r * 16 < rows)
-                  acc[t][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                      wv, __builtin_bit_cast(half8v, xv[r]), acc[t][r], 0, 0, 0);
-            }
+            for (int r = 0; r < RT; ++r)
+              if (r == 0 || r * 16 < rows) acc[t][r] = product(wv, xv[r], acc[t][r]);
           }
         }
       }
+    };
+    auto begin = [&](float (&f)[NT][STEPS][2]) {
+      __builtin_amdgcn_s_waitcnt(0);  // this wavefront's copies and weights have landed
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) w[t][s] = w_next[t][s];
+        e_next[t].exchange(col, grp, f[t]);
+      }
+      __syncthreads();  // the other wavefronts' copies too; the slab before is read
+    };
+
+    if (m0 != range.first) __syncthreads();  // the last rows' slabs are read
+    if (slab_lo < slab_whole) load(slab_lo);
+    for (int slab = slab_lo; slab < slab_whole; ++slab) {
+      float f[NT][STEPS][2];
+      begin(f);
+      if (slab + 1 < slab_whole) load(slab + 1);
+      multiply(slab, f);
+    }
+    if (slab_whole < slab_hi) {
+      const int left = (int)(k - (int64_t)slab_whole * KS);
+      copy(slab_whole);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint8_t* c = codes[t] + (int64_t)slab_whole * (KS / 2);
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+          const int at = s * 128 + grp * 32;
+          w_next[t][s] = (u32x4v){0, 0, 0, 0};
+          if (at + 32 <= left) {
+            w_next[t][s] = *(const u32x4v*)(c + s * 64);
+          } else if (!MX && at + 16 <= left) {
+            const u32x2v half = *(const u32x2v*)(c + s * 64);
+            w_next[t][s] = (u32x4v){half[0], half[1], 0, 0};
+          }
+        }
+        e_next[t].some(scales[t] + (int64_t)slab_whole * (KS / (MX ? 32 : 16)),
+                       left / (MX ? 32 : 16) - grp * ScaleLoad<MX, KS>::BYTES);
+      }
+      float f[NT][STEPS][2];
+      begin(f);
+      multiply(slab_whole, f);
     }
 
     // lane (col, grp) holds columns n0 + 16 t + 4 grp + i of row m0 + 16 r + col
@@ -432,28 +496,26 @@ __global__ __launch_bounds__(256) void linear_mfma(LinearArgs a, const uint16_t*
     for (int r = 0; r < RT; ++r) {
       const int64_t m = m0 + r * 16 + col;
       if (r * 16 + col >= rows) continue;
-      const float xs_inv = MX ? 1.0f : x_scale[m];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int64_t n = n0 + t * 16 + grp * 4;
         if (partial) {
-          float* to = partial + ((int64_t)split * a.rows + m) * a.n + n;
-          const float4v v = acc[t][r] * xs_inv;
+          float* to = partial + (split * a.rows + m) * a.n + n;
           if (n + 4 <= a.n && a.n % 4 == 0) {
-            *(float4v*)to = v;
+            *(float4v*)to = acc[t][r];
           } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (n + i < a.n) to[i] = v[i];
+              if (n + i < a.n) to[i] = acc[t][r][i];
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (n + i < a.n) {
-              const float s = MX ? 1.0f : a.row_scales[matrix * a.n + n + i];
-              put_out(a, m * a.n + n + i, acc[t][r][i] * xs_inv * s);
-            }
+          continue;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < a.n) {
+            const float s = MX ? 1.0f : a.row_scales[matrix * a.n + n + i];
+            put_out(a, m * a.n + n + i, acc[t][r][i] * s);
+          }
       }
     }
     if (!a.offsets) break;
@@ -467,6 +529,7 @@ __global__ __launch_bounds__(256) void linear_join(LinearArgs a, int splits,
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, all = a.rows * a.n;
   if (at >= all) return;
   float sum = 0.0f;
+#pragma unroll 4
   for (int s = 0; s < splits; ++s) sum += partial[s * all + at];
   put_out(a, at, MX ? sum : sum * a.row_scales[at % a.n]);
 }
@@ -475,64 +538,61 @@ __global__ __launch_bounds__(256) void linear_join(LinearArgs a, int splits,
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+enum class Form { kDot, kSmall, kLarge };
+
 struct Plan {
-  int dot_rows;  // rows of the dot form (1, 2, 4), 0: the matrix form
-  int rt, nt;
+  Form form;
+  int rows;  // rows a workgroup takes: 1, 2 (dot), 16, 32, 64
+  int nt;    // column tiles a wavefront takes: 1, 2
   int64_t splits;
 };
 
-#ifndef DOT_W
-#define DOT_W 4
-#endif
-#ifndef DOT_NC1
-#define DOT_NC1 2
-#endif
-#ifndef LIN_TARGET
-#define LIN_TARGET 512
-#endif
-#ifndef LIN_NT1
-#define LIN_NT1 1
-#endif
-
+// The forms' times below are for NVFP4, on the device, in us.
 Plan plan_of(int64_t rows, int64_t n, int64_t k, int64_t groups) {
-  Plan p{0, 1, 1, 1};
-  if (groups == 0 && rows <= 4) {
-    p.dot_rows = rows <= 2 ? (int)rows : 4;
+  Plan p{Form::kLarge, 16, 1, 1};
+  if (groups == 0 && rows <= 2) {
+    p.form = Form::kDot;
+    p.rows = (int)rows;
+    // one column a wavefront fills the chip best (2048 x 7168: 5.2, 5.8 with two); where
+    // columns abound, two share the activations' reads (65536 x 7168: 50, 56 with one)
+    p.nt = rows == 2 || n >= 16384 ? 2 : 1;
     return p;
   }
-  const int64_t each = groups ? ceil_div(rows, groups) : rows;
-  p.rt = each <= 16 ? 1 : each <= 32 ? 2 : 4;
-  p.nt = p.rt == 1 ? LIN_NT1 : 2;
-  if (groups == 0) {
-    const int64_t tiles = ceil_div(n, 64 * p.nt) * ceil_div(rows, 16 * p.rt);
-    const int64_t slabs = ceil_div(k, p.rt == 1 ? 512 : 256);
-    p.splits = ceil_div(LIN_TARGET, tiles);
-    if (p.splits > slabs) p.splits = slabs;
-    if (p.splits > 16) p.splits = 16;
+  // with groups, enough rows for most of them in one pass over their weights: routing leaves
+  // a group's share mostly below its mean and twice the mean's root
+  int64_t each = groups ? ceil_div(rows, groups) : rows, root = 1;
+  while (root * root < each) ++root;
+  if (groups) each = each + 2 * root < rows ? each + 2 * root : rows;
+  p.rows = each <= 16 ? 16 : each <= 32 ? 32 : 64;
+  if (groups) {
+    p.nt = p.rows == 16 ? 1 : 2;
+    return p;
   }
+  // Each wavefront of the small form goes through k / 1024 steps a row tile on its own, and
+  // reads all activations: 8 rows, 4096 x 4096 6.6 (large form 9.0), 2048 x 2048 4.4 (7.9),
+  // but 1024 x 7168 9.2 (8.7), 16384 x 2048 11.4 (11.3); 24 rows, 2048 x 2048 6.3 (7.3), but
+  // 7168 x 2048 10.5 (9.6)
+  const int64_t row_tiles = ceil_div(rows, 16);
+  if (k * row_tiles <= 4096 && n * k * row_tiles <= ((int64_t)1 << 24)) {
+    p.form = Form::kSmall;
+    return p;
+  }
+  // above 16 rows, two column tiles a wavefront halve the activations' reads from LDS where
+  // enough workgroups remain (64 rows, 65536 x 7168: 103, 124 with one; 8192 x 7168: 24.7, 22.5)
+  p.nt = p.rows > 16 && n >= 16384 ? 2 : 1;
+  // k divided over enough workgroups to fill the chip twice, each two slabs at least
+  const int64_t tiles = ceil_div(n, 64 * p.nt) * ceil_div(rows, p.rows);
+  const int64_t slabs = ceil_div(k, p.rows == 16 ? 512 : 256);
+  p.splits = ceil_div(512, tiles);
+  if (p.splits > slabs / 2) p.splits = slabs / 2;
+  if (p.splits > 16) p.splits = 16;
+  if (p.splits < 1) p.splits = 1;
   return p;
-}
-
-// Workspace: NVFP4's converted activations and their scales, then the
-// splits' partial sums, each from a 16-byte boundary.
-int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
-
-struct Space {
-  int64_t scale, partial, bytes;
-};
-
-Space space_of(bool mx, const Plan& p, int64_t rows, int64_t n, int64_t k) {
-  Space s{0, 0, 0};
-  if (p.dot_rows) return s;
-  s.scale = mx ? 0 : round16(rows * k * 2);
-  s.partial = mx ? 0 : s.scale + round16(rows * 4);
-  s.bytes = s.partial + (p.splits > 1 ? p.splits * rows * n * 4 : 0);
-  return s;
 }
 
 // The dispatch packet counts work-items in 32 bits, and the second grid
 // dimension 16: larger calls go in several launches.
-constexpr int64_t kMaxBlocks = ((int64_t)1 << 31) / 256;
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 31) / 512;
 
 template <bool MX, int ROWS, int NC, int WAVES>
 hipError_t dot(const LinearArgs& a, hipStream_t stream) {
@@ -546,21 +606,16 @@ hipError_t dot(const LinearArgs& a, hipStream_t stream) {
   return hipSuccess;
 }
 
+template <bool MX, int RT, int WAVES>
+hipError_t small(const LinearArgs& a, hipStream_t stream) {
+  const dim3 grid((uint32_t)ceil_div(a.n, 16), (uint32_t)ceil_div(a.rows, 16 * RT));
+  linear_small<MX, RT, WAVES><<<grid, 64 * WAVES, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
 template <bool MX, int RT, int NT>
-hipError_t mfma(const LinearArgs& a, const Plan& p, hipStream_t stream) {
-  const Space space = space_of(MX, p, a.rows, a.n, a.k);
-  uint8_t* ws = (uint8_t*)a.workspace;
-  const uint16_t* x = MX ? (const uint16_t*)a.x : (const uint16_t*)ws;
-  float* x_scale = MX ? nullptr : (float*)(ws + space.scale);
-  if (!MX) {
-    for (int64_t r0 = 0; r0 < a.rows; r0 += kMaxBlocks) {
-      const int64_t n = a.rows - r0 < kMaxBlocks ? a.rows - r0 : kMaxBlocks;
-      linear_convert<<<(uint32_t)n, 256, 0, stream>>>(a, r0, (uint16_t*)ws, x_scale);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
-  }
-  float* partial = p.splits > 1 ? (float*)(ws + space.partial) : nullptr;
+hipError_t large(const LinearArgs& a, const Plan& p, hipStream_t stream) {
+  float* partial = p.splits > 1 ? (float*)a.workspace : nullptr;
   const int64_t xs = ceil_div(a.n, 64 * NT);
   const int64_t ys = a.groups ? a.groups : ceil_div(a.rows, 16 * RT);
   const int64_t dx = xs < kMaxBlocks / p.splits ? xs : kMaxBlocks / p.splits;
@@ -570,8 +625,7 @@ hipError_t mfma(const LinearArgs& a, const Plan& p, hipStream_t stream) {
     for (int64_t x0 = 0; x0 < xs; x0 += dx) {
       const dim3 grid((uint32_t)(xs - x0 < dx ? xs - x0 : dx),
                       (uint32_t)(ys - y0 < dy ? ys - y0 : dy), (uint32_t)p.splits);
-      linear_mfma<MX, RT, NT><<<grid, 256, 0, stream>>>(a, x, x_scale, x0, y0, (int)p.splits,
-                                                        partial);
+      linear_large<MX, RT, NT><<<grid, 256, 0, stream>>>(a, x0, y0, partial);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
@@ -585,18 +639,27 @@ hipError_t mfma(const LinearArgs& a, const Plan& p, hipStream_t stream) {
 template <bool MX>
 hipError_t launch(const LinearArgs& a, hipStream_t stream) {
   const Plan p = plan_of(a.rows, a.n, a.k, a.groups);
-  if (p.dot_rows == 1) return dot<MX, 1, DOT_NC1, DOT_W>(a, stream);
-  if (p.dot_rows == 2) return dot<MX, 2, 2, DOT_W>(a, stream);
-  if (p.dot_rows == 4) return dot<MX, 4, 2, DOT_W>(a, stream);
-  if (p.rt == 1) return mfma<MX, 1, LIN_NT1>(a, p, stream);
-  if (p.rt == 2) return mfma<MX, 2, 2>(a, p, stream);
-  return mfma<MX, 4, 2>(a, p, stream);
+  switch (p.form) {
+    case Form::kDot:
+      if (p.rows == 2) return dot<MX, 2, 2, 4>(a, stream);
+      return p.nt == 2 ? dot<MX, 1, 2, 4>(a, stream) : dot<MX, 1, 1, 8>(a, stream);
+    case Form::kSmall:
+      if (p.rows == 16) return small<MX, 1, 8>(a, stream);
+      if (p.rows == 32) return small<MX, 2, 8>(a, stream);
+      return small<MX, 4, 8>(a, stream);
+    default:
+      if (p.rows == 16) return large<MX, 1, 1>(a, p, stream);
+      if (p.rows == 32)
+        return p.nt == 2 ? large<MX, 2, 2>(a, p, stream) : large<MX, 2, 1>(a, p, stream);
+      return p.nt == 2 ? large<MX, 4, 2>(a, p, stream) : large<MX, 4, 1>(a, p, stream);
+  }
 }
 
 }  // namespace
 
-int64_t linear_workspace_bytes(bool mx, int64_t rows, int64_t n, int64_t k, int64_t groups) {
-  return space_of(mx, plan_of(rows, n, k, groups), rows, n, k).bytes;
+int64_t linear_workspace_bytes(bool, int64_t rows, int64_t n, int64_t k, int64_t groups) {
+  const Plan p = plan_of(rows, n, k, groups);
+  return p.splits > 1 ? p.splits * rows * n * 4 : 0;
 }
 
 hipError_t linear_launch(bool mx, const LinearArgs& a, hipStream_t stream) {

@@ -29,12 +29,10 @@ extern "C" {
 
 /*
  * nvfp4_linear -- y = x . DQ(W)^T for NVFP4 weights (the outputs of
- * nvfp4_quantize for W): y[m][j] = sum_i x[m][i] * (+-g(code) * e * s_j),
- * the weights' values taken exactly, summed in FP32, times s_j, rounded
- * once to the output type.
+ * nvfp4_quantize for W): y[m][j] = s_j * sum_i x[m][i] * (+-g(code) * e),
+ * products of exact values summed in FP32, rounded once to the output type.
  *
- *   x             BF16 [rows, k], 16-byte aligned.  Elements below 2^-39 of
- *                 their row's largest magnitude may count as zero.
+ *   x             BF16 [rows, k], 16-byte aligned.
  *   codes         uint8 [n, k/2] ([num_groups, n, k/2] with groups), 8-byte
  *                 aligned; block_scales uint8 [.., n, k/16] (E4M3FN);
  *                 row_scales float [.., n], 4-byte aligned.
