@@ -169,33 +169,50 @@ __global__ __launch_bounds__(256) void kv_append_kernel(CacheView c, const uint1
   if (block == 0) c.token_scales[which][p.row] = s;
 }
 
-__global__ __launch_bounds__(256) void kv_read_kernel(CacheView c, Divisor blocks,
-                                                      const int64_t* slots, uint32_t units,
+// PIECES half blocks (8 elements) a thread, 256 apart: a wavefront's stores
+// are 1 KiB of consecutive BF16 each, and several loads, each behind that of
+// its slot, are in flight.  Non-temporal stores: 32k tokens of 8 heads of 128
+// take 31 us (5.5 TB/s), 42 with plain ones, and 47 with a whole block a
+// thread, whose stores fill every line in two instructions.
+template <int PIECES>
+__global__ __launch_bounds__(256) void kv_read_kernel(CacheView c, Divisor row_pieces,
+                                                      const int64_t* slots, uint32_t pieces,
                                                       u32x4v* k_out, u32x4v* v_out) {
   const int which = blockIdx.y;
-  const uint32_t unit = blockIdx.x * 256 + threadIdx.x;  // a 16-element block
-  if (unit >= units) return;
-  const uint32_t row = quotient(unit, blocks), token = quotient(row, c.heads);
-  const int block = (int)(unit - row * blocks.d);
-  const int64_t slot = slots[token];
-  u32x4v w[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-  if (slot >= 0 && slot < c.slots) {
-    const Place p = place_of(c, (uint32_t)slot, row - token * c.heads.d, block, which);
-    const u32x2v q = ((const u32x2v*)c.codes[which])[p.row * c.blocks + block];
-    const float e = e4m3_value<0>(c.scales[which][p.scale]);
-    const float s = c.token_scales[which][p.row];
+  const uint32_t piece0 = blockIdx.x * (256 * PIECES) + threadIdx.x;
+  uint32_t q[PIECES], e[PIECES];
+  float s[PIECES];
+  int64_t slot[PIECES];
+  uint32_t row[PIECES], token[PIECES];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float2v g[4] = {e2m1x2_values<0>(q[h]), e2m1x2_values<1>(q[h]),
-                            e2m1x2_values<2>(q[h]), e2m1x2_values<3>(q[h])};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[h][i] = cvt_bf16x2((g[i][0] * e) * s, (g[i][1] * e) * s);
-    }
+  for (int i = 0; i < PIECES; ++i) {
+    row[i] = quotient(min(piece0 + i * 256, pieces - 1), row_pieces);
+    token[i] = quotient(row[i], c.heads);
+    slot[i] = slots[token[i]];
   }
-  u32x4v* out = (which ? v_out : k_out) + (int64_t)unit * 2;
-  out[0] = w[0];
-  out[1] = w[1];
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int in_row = (int)(min(piece0 + i * 256, pieces - 1) - row[i] * row_pieces.d);
+    const bool held = slot[i] >= 0 && slot[i] < c.slots;  // else zeros, from slot 0's place
+    const Place p = place_of(c, held ? (uint32_t)slot[i] : 0u, row[i] - token[i] * c.heads.d,
+                             in_row / 2, which);
+    q[i] = ((const uint32_t*)c.codes[which])[p.row * row_pieces.d + in_row];
+    e[i] = c.scales[which][p.scale];
+    s[i] = c.token_scales[which][p.row];
+    if (!held) q[i] = 0, e[i] = 0, s[i] = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const uint32_t piece = piece0 + i * 256;
+    if (piece >= pieces) return;
+    const float f = e4m3_value<0>(e[i]);
+    const float2v g[4] = {e2m1x2_values<0>(q[i]), e2m1x2_values<1>(q[i]),
+                          e2m1x2_values<2>(q[i]), e2m1x2_values<3>(q[i])};
+    u32x4v w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = cvt_bf16x2((g[j][0] * f) * s[i], (g[j][1] * f) * s[i]);
+    __builtin_nontemporal_store(w, (which ? v_out : k_out) + piece);
+  }
 }
 
 }  // namespace
@@ -242,13 +259,22 @@ hipError_t kv_append_launch(const KvCache& cache, const void* k, int64_t k_strid
 hipError_t kv_read_launch(const KvCache& cache, const int64_t* slots, int64_t tokens, void* k_out,
                           void* v_out, hipStream_t stream) {
   const CacheView c = view_of(cache);
-  const int64_t per_token = cache.kv_heads * c.blocks, step = tokens_per_launch(per_token);
+  const int64_t per_token = cache.kv_heads * c.blocks * 2, step = tokens_per_launch(per_token);
+  const Divisor row_pieces = divisor_of((uint32_t)c.blocks * 2);
   for (int64_t t0 = 0; t0 < tokens; t0 += step) {
-    const int64_t units = (tokens - t0 < step ? tokens - t0 : step) * per_token;
-    const dim3 g((uint32_t)((units + 255) / 256), 2);
-    kv_read_kernel<<<g, 256, 0, stream>>>(c, divisor_of((uint32_t)c.blocks), slots + t0,
-                                          (uint32_t)units, (u32x4v*)k_out + t0 * per_token * 2,
-                                          (u32x4v*)v_out + t0 * per_token * 2);
+    const int64_t pieces = (tokens - t0 < step ? tokens - t0 : step) * per_token;
+    u32x4v* ko = (u32x4v*)k_out + t0 * per_token;
+    u32x4v* vo = (u32x4v*)v_out + t0 * per_token;
+    // 32k tokens of 8 heads of 128: 31 us with 4 pieces a thread, 33 with 2, 56 with 1; 64
+    // tokens (with their append): 5.9, 5.3 and 5.4
+    const int each = pieces >= ((int64_t)1 << 19) ? 4 : 2;
+    const dim3 g((uint32_t)((pieces + 256 * each - 1) / (256 * each)), 2);
+    if (each == 4)
+      kv_read_kernel<4>
+          <<<g, 256, 0, stream>>>(c, row_pieces, slots + t0, (uint32_t)pieces, ko, vo);
+    else
+      kv_read_kernel<2>
+          <<<g, 256, 0, stream>>>(c, row_pieces, slots + t0, (uint32_t)pieces, ko, vo);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
