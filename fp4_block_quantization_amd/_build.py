@@ -28,6 +28,8 @@ EXACTDECISION_PATH = os.path.join(BUILD_DIR, "libfp4q_exactdecision.so")
 MEMBENCH_PATH = os.path.join(BUILD_DIR, "libfp4q_membench.so")
 # the rollout engine's operators (include/fp4q/rollout.h)
 ROLLOUT_PATH = os.path.join(BUILD_DIR, "libfp4q_rollout.so")
+# and the native half of their Python binding (host code only)
+ROLLOUT_EXT_PATH = os.path.join(BUILD_DIR, "fp4q_rollout_ext.so")
 CSRC_ROLLOUT = os.path.join(HERE, "csrc_rollout")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -78,13 +80,35 @@ def build_rollout(verbose: bool = False) -> str:
     return build(verbose, out_path=ROLLOUT_PATH, sources=ROLLOUT_SOURCES, src_dir=CSRC_ROLLOUT)
 
 
+def build_rollout_ext(verbose: bool = False) -> str:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    tmp = ROLLOUT_EXT_PATH + ".tmp%d" % os.getpid()
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    includes = cpp_extension.include_paths() + [sysconfig.get_paths()["include"],
+                                                os.path.join(ROOT, "include")]
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           *[a for i in includes for a in ("-isystem", i)],
+           os.path.join(CSRC_ROLLOUT, "rollout_ext.cpp"), "-L" + lib, "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, ROLLOUT_EXT_PATH)
+    return ROLLOUT_EXT_PATH
+
+
 def build_all(verbose: bool = False):
-    """libfp4q.so, its stand-in and exact-decision builds, the K0 probes and
-    libfp4q_rollout.so."""
+    """libfp4q.so, its stand-in and exact-decision builds, the K0 probes,
+    libfp4q_rollout.so and its binding's native half."""
     return [build(verbose), build(verbose, ["-DFP4Q_STANDIN=1"], STANDIN_PATH),
             build(verbose, ["-DFP4Q_NV_CERTIFY=0"], EXACTDECISION_PATH),
             build(verbose, out_path=MEMBENCH_PATH, sources=MEMBENCH_SOURCES),
-            build_rollout(verbose)]
+            build_rollout(verbose), build_rollout_ext(verbose)]
 
 
 if __name__ == "__main__":
