@@ -35,6 +35,7 @@
 // unequal contexts fills the chip as an equal one does.  A second kernel
 // joins the parts of an item in a fixed order.
 #include "fp4q_device.h"
+#include "rollout_divisor.h"
 #include "rollout_launch.h"
 
 namespace fp4q {
@@ -75,7 +76,10 @@ struct Params {
   float* next_o;       // [parts][16 * RT][D]
   float2* next_ml;
   int64_t q_stride, rows;
-  int32_t num_pages, page_size, page_groups, kv_heads, per_head;  // per_head: q_heads / kv_heads
+  Divisor page_groups;  // 16-token groups of a page
+  Divisor per_head;     // q_heads / kv_heads
+  Divisor per_seq;      // query rows of a sequence and cache head: q_tokens * per_head
+  int32_t num_pages, page_size, kv_heads;
   int32_t batch, q_tokens, q_heads, max_pages, max_prefix_pages, groups;
   int32_t blocks;  // row blocks of a sequence's own items
   int32_t parts;   // parts to cut all items into, about; 0: one workgroup per item
@@ -129,6 +133,7 @@ __device__ __forceinline__ int64_t lane_value(int64_t v, int from) {
 // of one page-table row that they see.
 struct Item {
   const int32_t* table;
+  int32_t pages;    // entries of that row
   int32_t len;      // tokens any row of the block sees
   int32_t floor;    // tokens every row of the block sees
   int32_t first_b;  // row r belongs to sequence first_b + (row0 + r) / (T * per_head)
@@ -139,11 +144,16 @@ struct Item {
   bool prefix;
 };
 
-__device__ __forceinline__ int64_t global_row(const Params& p, const Item& j, int r) {
-  const int per_seq = p.q_tokens * p.per_head;
-  const int rr = j.row0 + r, b = rr / per_seq, in = rr - b * per_seq;
-  const int t = in / p.per_head, g = in - t * p.per_head;
-  return ((int64_t)(j.first_b + b) * p.q_tokens + t) * p.q_heads + j.kvh * p.per_head + g;
+struct Row {
+  int64_t token;  // b * q_tokens + t
+  int t, head;
+};
+
+__device__ __forceinline__ Row row_of(const Params& p, const Item& j, int r) {
+  const uint32_t rr = j.row0 + r, b = quotient(rr, p.per_seq), in = rr - b * p.per_seq.d;
+  const uint32_t t = quotient(in, p.per_head);
+  return Row{(int64_t)(j.first_b + (int)b) * p.q_tokens + t, (int)t,
+             j.kvh * (int)p.per_head.d + (int)(in - t * p.per_head.d)};
 }
 
 __device__ __forceinline__ int tiles_of(int len) { return (int)((uint32_t)(len + kTile - 1) / kTile); }
@@ -155,8 +165,8 @@ __device__ __forceinline__ int32_t own_length(const Params& p, int b) {
 // Tokens that row block rb of a sequence of own_len tokens sees.
 template <int RB>
 __device__ __forceinline__ int seen_by(const Params& p, int own_len, int rb) {
-  const int last = min((rb + 1) * RB, p.q_tokens * p.per_head) - 1;
-  return max(0, own_len - p.q_tokens + 1 + last / p.per_head);
+  const uint32_t last = min((uint32_t)(rb + 1) * RB, p.per_seq.d) - 1;
+  return max(0, own_len - p.q_tokens + 1 + (int)quotient(last, p.per_head));
 }
 
 struct Members {
@@ -182,7 +192,7 @@ template <int RB, class F>
 __device__ __forceinline__ void items_of(const Params& p, int entry, F f) {
   if (entry < p.groups) {
     const Members m = members_of(p, entry);
-    const int rows = (m.hi - m.lo) * p.q_tokens * p.per_head;
+    const int rows = (m.hi - m.lo) * (int)p.per_seq.d;
     const int tiles = tiles_of(prefix_length(p, entry));
     if (tiles > 0) f((rows + RB - 1) / RB * p.kv_heads, tiles);
     return;
@@ -208,39 +218,66 @@ struct Spot {
   int share;
 };
 
-// The entry of part blockIdx.x.  The workgroup's 256 threads sum the tiles
-// of all entries, which gives the part's length, and then scan the entries'
-// counts of parts.  All sums fit in 31 bits (the host's check).
+// The entry of part blockIdx.x: the tiles of all entries are summed, which
+// gives the parts' length, and then the entries' counts of parts are scanned.
+// All sums fit in 31 bits (the host's check).  Up to 64 entries, one a lane,
+// every wavefront does it by itself: this stands before anything else that a
+// workgroup does, and a barrier costs more than the repetition.
 template <int RB>
 __device__ __forceinline__ Spot find_part(const Params& p, int (&shared)[16]) {
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  const int entries = p.groups + p.batch, each = (entries + 255) / 256;
-  const int lo = min(tid * each, entries), hi = min(lo + each, entries);
-  int tiles = 0;
-  for (int e = lo; e < hi; ++e) items_of<RB>(p, e, [&](int n, int each_tiles) { tiles += n * each_tiles; });
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) tiles += __shfl_xor(tiles, s);
-  if (lane == 0) shared[wave] = tiles;
-  __syncthreads();
+  const int entries = p.groups + p.batch, want = (int)blockIdx.x;
   Spot spot;
-  spot.share = part_tiles((uint32_t)(shared[0] + shared[1] + shared[2] + shared[3]),
-                          (uint32_t)p.parts);
-  // counts of parts, and of items
   int parts = 0, items = 0;
   auto count = [&](int n, int each_tiles) {
     parts += n * parts_of(each_tiles, spot.share);
     items += n;
   };
-  for (int e = lo; e < hi; ++e) items_of<RB>(p, e, count);
-  int parts_upto = parts, items_upto = items;
+  auto scan = [&](int& parts_upto, int& items_upto) {
+    parts_upto = parts, items_upto = items;
 #pragma unroll
-  for (int s = 1; s < 64; s *= 2) {
-    const int a = __shfl_up(parts_upto, s), b = __shfl_up(items_upto, s);
-    if (lane >= s) {
-      parts_upto += a;
-      items_upto += b;
+    for (int s = 1; s < 64; s *= 2) {
+      const int a = __shfl_up(parts_upto, s), b = __shfl_up(items_upto, s);
+      if (lane >= s) {
+        parts_upto += a;
+        items_upto += b;
+      }
     }
+  };
+  auto sum_tiles = [&](int lo, int hi) {
+    int tiles = 0;
+    for (int e = lo; e < hi; ++e)
+      items_of<RB>(p, e, [&](int n, int each_tiles) { tiles += n * each_tiles; });
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) tiles += __shfl_xor(tiles, s);
+    return tiles;
+  };
+  int parts_upto, items_upto;
+  if (entries <= 64) {
+    const int lo = min(lane, entries), hi = min(lane + 1, entries);
+    spot.share = part_tiles((uint32_t)sum_tiles(lo, hi), (uint32_t)p.parts);
+    if (lo < hi) items_of<RB>(p, lo, count);
+    scan(parts_upto, items_upto);
+    const uint64_t past = __ballot(parts_upto > want);
+    if (past == 0) {
+      spot.entry = -1;
+      return spot;
+    }
+    spot.entry = __builtin_ctzll(past);
+    spot.parts_before = __builtin_amdgcn_readlane(parts_upto - parts, spot.entry);
+    spot.further_before =
+        spot.parts_before - __builtin_amdgcn_readlane(items_upto - items, spot.entry);
+    return spot;
   }
+  const int each = (entries + 255) / 256;
+  const int lo = min(tid * each, entries), hi = min(lo + each, entries);
+  const int tiles = sum_tiles(lo, hi);
+  if (lane == 0) shared[wave] = tiles;
+  __syncthreads();
+  spot.share = part_tiles((uint32_t)(shared[0] + shared[1] + shared[2] + shared[3]),
+                          (uint32_t)p.parts);
+  for (int e = lo; e < hi; ++e) items_of<RB>(p, e, count);
+  scan(parts_upto, items_upto);
   if (lane == 63) {
     shared[4 + wave] = parts_upto;
     shared[8 + wave] = items_upto;
@@ -255,7 +292,6 @@ __device__ __forceinline__ Spot find_part(const Params& p, int (&shared)[16]) {
       items_before += shared[8 + w];
     }
   }
-  const int want = (int)blockIdx.x;
   if (want >= before && want < before + parts) {
     int e = lo;
     for (;; ++e) {
@@ -315,52 +351,6 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int col = lane % 16, grp = lane / 16;
   const int steps = max(0, min(tile_hi, tiles_of(job.len)) - tile_lo - wave + WAVES - 1) / WAVES;
-  const int last_group = (job.len - 1) / 16;
-
-  // queries: lane (col, grp) holds row col's elements [grp * D/4, (grp + 1) * D/4)
-  half8v q[RT][NK];
-  float c_q[RT];
-  int limit[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int r = rt * 16 + col;
-    const bool live = r < job.rows;
-    const int rr = job.row0 + (live ? r : 0);
-    limit[rt] = job.prefix ? job.len
-                           : job.own_len - p.q_tokens + 1 + rr / p.per_head;
-    u32x4v raw[NK];
-    const int64_t row = global_row(p, job, live ? r : 0);
-    const int64_t bt = row / p.q_heads;
-    const uint16_t* src = p.q + bt * p.q_stride + (row - bt * p.q_heads) * D + grp * (D / 4);
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < NK; ++k) {
-      raw[k] = live ? ((const u32x4v*)src)[k] : (u32x4v){0, 0, 0, 0};
-      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
-    }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-    // 2^ex: the row's largest element lands in [2^14, 2^15).  A row of zeros, or one
-    // with a NaN or infinity, stays as it is
-    const int field = (int)(top >> 7);
-    const int ex = top == 0 || field == 255 ? 0 : 14 + 127 - max(field, 1);
-    const float sign = p.scale < 0.0f ? -1.0f : 1.0f;
-    // (never 0, so that a masked score's -infinity stays one)
-    c_q[rt] = p.scale == 0.0f ? 0x1p-149f
-                              : __builtin_ldexpf(__builtin_fabsf(p.scale) * kLog2e, -ex);
-#pragma unroll
-    for (int k = 0; k < NK; ++k) {
-      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        q[rt][k][2 * i] = (_Float16)__builtin_ldexpf(bf16_lo(w[i]) * sign, ex);
-        q[rt][k][2 * i + 1] = (_Float16)__builtin_ldexpf(bf16_hi(w[i]) * sign, ex);
-      }
-    }
-  }
-
   float4v o[RT][DT];
   float m[RT], l[RT];
 #pragma unroll
@@ -378,8 +368,11 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
   int64_t page_row = 0, page_scale = 0;
   auto load_pages = [&](int first_step) {
     const int tile = tile_lo + wave + (first_step + lane / 4) * WAVES;
-    const int g = min(tile * 4 + lane % 4, last_group);
-    const int page = g / p.page_groups, at = (g - page * p.page_groups) * 16;
+    // (past the context's end: whatever the table holds there, clamped, and masked later; so
+    // the first load need not wait for the context's length)
+    const uint32_t g = min((uint32_t)tile * 4 + lane % 4, (uint32_t)job.pages * p.page_groups.d - 1);
+    const uint32_t page = quotient(g, p.page_groups);
+    const int at = (int)(g - page * p.page_groups.d) * 16;
     const int id = min(max(job.table[page], 0), p.num_pages - 1);
     const int64_t head = ((int64_t)id * p.kv_heads + job.kvh) * p.page_size;
     page_row = head + at;
@@ -469,11 +462,53 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
     return __builtin_amdgcn_ds_read_tr4_b64_v2i32(
         (__attribute__((address_space(3))) int2v*)(tile.codes + turned * kVRow + dt * 8));
   };
+  // The page table, the queries and the first tile are asked for before anything is done
+  // with them.  Queries: lane (col, grp) holds row col's elements [grp D/4, (grp + 1) D/4).
+  u32x4v raw[RT][NK];
+  int limit[RT];
+  if (job.pages > 0) load_pages(0);
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const bool live = rt * 16 + col < job.rows;
+    const int r = live ? rt * 16 + col : 0;
+    const Row row = row_of(p, job, r);
+    const uint16_t* src = p.q + row.token * p.q_stride + (int64_t)row.head * D + grp * (D / 4);
+    limit[rt] = job.prefix ? job.len : job.own_len - p.q_tokens + 1 + row.t;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) raw[rt][k] = live ? ((const u32x4v*)src)[k] : (u32x4v){0, 0, 0, 0};
+  }
   if (steps > 0) {
-    load_pages(0);
     locate(0);
     load_values(0);
     load_keys(0);
+  }
+  half8v q[RT][NK];
+  float c_q[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        top = max(top, max(raw[rt][k][i] & 0x7FFFu, raw[rt][k][i] >> 16 & 0x7FFFu));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+    // 2^ex: the row's largest element lands in [2^14, 2^15).  A row of zeros, or one
+    // with a NaN or infinity, stays as it is
+    const int field = (int)(top >> 7);
+    const int ex = top == 0 || field == 255 ? 0 : 14 + 127 - max(field, 1);
+    const float sign = p.scale < 0.0f ? -1.0f : 1.0f;
+    // (never 0, so that a masked score's -infinity stays one)
+    c_q[rt] = p.scale == 0.0f ? 0x1p-149f
+                              : __builtin_ldexpf(__builtin_fabsf(p.scale) * kLog2e, -ex);
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        q[rt][k][2 * i] = (_Float16)__builtin_ldexpf(bf16_lo(raw[rt][k][i]) * sign, ex);
+        q[rt][k][2 * i + 1] = (_Float16)__builtin_ldexpf(bf16_hi(raw[rt][k][i]) * sign, ex);
+      }
   }
   for (int step = 0; step < steps; ++step) {
     const int t0 = (tile_lo + wave + step * WAVES) * kTile;
@@ -651,7 +686,8 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
         f[w] = factor(sh.merge.ml[w][row_in].x, base);
         total += f[w] * sh.merge.ml[w][row_in].y;
       }
-      const int64_t row = global_row(p, job, r);
+      const Row of = row_of(p, job, r);
+      const int64_t row = of.token * p.q_heads + of.head;
       const int64_t next = (int64_t)next_part * RB + r;
       float* to = tile_lo > 0 ? p.next_o + next * D : p.first_o[job.prefix] + row * D;
       const float inv = total == 0.0f ? 0.0f : 1.0f / total;
@@ -687,11 +723,12 @@ __device__ __forceinline__ void own_item(const Params& p, int b, int rb, Item& j
   j.prefix = false;
   j.first_b = b;
   j.row0 = rb * RB;
-  j.rows = min(RB, p.q_tokens * p.per_head - j.row0);
+  j.rows = min(RB, (int)p.per_seq.d - j.row0);
   j.table = p.page_table + (int64_t)b * p.max_pages;
+  j.pages = p.max_pages;
   j.own_len = own_length(p, b);
   j.len = seen_by<RB>(p, j.own_len, rb);
-  j.floor = max(0, j.own_len - p.q_tokens + 1 + j.row0 / p.per_head);
+  j.floor = max(0, j.own_len - p.q_tokens + 1 + (int)quotient(j.row0, p.per_head));
 }
 
 // The same value in every lane, said so: descriptors and branches come from it.
@@ -736,9 +773,10 @@ __global__ __launch_bounds__(256, groups_per_cu(D, RT)) void attention_parts(Par
   int tiles, item, n;
   if (entry < p.groups) {
     const Members m = members_of(p, entry);
-    const int rows = (m.hi - m.lo) * p.q_tokens * p.per_head, blocks = (rows + RB - 1) / RB;
+    const int rows = (m.hi - m.lo) * (int)p.per_seq.d, blocks = (rows + RB - 1) / RB;
     job.prefix = true;
     job.table = p.prefix_table + (int64_t)entry * p.max_prefix_pages;
+    job.pages = p.max_prefix_pages;
     job.len = job.floor = job.own_len = prefix_length(p, entry);
     tiles = tiles_of(job.len);
     n = parts_of(tiles, share);
@@ -791,7 +829,8 @@ __global__ __launch_bounds__(256) void attention_join(Params p) {
   const First own = p.first[0][row];
   if (own.more < 0) return;  // written whole
   const int b = (int)(bt / p.q_tokens), t = (int)(bt - (int64_t)b * p.q_tokens);
-  const int kvh = head / p.per_head, in_seq = t * p.per_head + head - kvh * p.per_head;
+  const int kvh = (int)quotient(head, p.per_head);
+  const int in_seq = (t - kvh) * (int)p.per_head.d + head;
 
   float top = -INFINITY, total = 0.0f;
   float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -827,7 +866,7 @@ __global__ __launch_bounds__(256) void attention_join(Params p) {
       const Members m = members_of(p, lo - 1);
       if (b >= m.lo && b < m.hi && prefix_length(p, lo - 1) > 0)
         gather(p.first[1][row], p.first_o[1] + row * D,
-               ((b - m.lo) * p.q_tokens * p.per_head + in_seq) % RB);
+               ((b - m.lo) * (int)p.per_seq.d + in_seq) % RB);
     }
   }
   gather(own, p.first_o[0] + row * D, in_seq % RB);
@@ -980,9 +1019,10 @@ hipError_t kv_attention_launch(const KvCache& c, const AttentionArgs& a, hipStre
   p.rows = plan.rows;
   p.num_pages = (int32_t)c.num_pages;
   p.page_size = (int32_t)c.page_size;
-  p.page_groups = (int32_t)(c.page_size / 16);
   p.kv_heads = (int32_t)c.kv_heads;
-  p.per_head = (int32_t)(a.q_heads / c.kv_heads);
+  p.page_groups = divisor_of((uint32_t)(c.page_size / 16));
+  p.per_head = divisor_of((uint32_t)(a.q_heads / c.kv_heads));
+  p.per_seq = divisor_of((uint32_t)(a.q_tokens * (a.q_heads / c.kv_heads)));
   p.batch = (int32_t)a.batch;
   p.q_tokens = (int32_t)a.q_tokens;
   p.q_heads = (int32_t)a.q_heads;
