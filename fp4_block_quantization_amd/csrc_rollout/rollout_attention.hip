@@ -333,7 +333,7 @@ struct Shared {
 
 // Workgroups of four wavefronts that a CU holds (by registers).
 constexpr int groups_per_cu(int d, int rt) {
-  return rt == 1 ? (d == 64 ? 4 : d == 128 ? 3 : 2) : (d <= 128 ? 2 : 1);
+  return rt == 1 && d <= 128 ? (d == 64 ? 4 : 3) : 2;
 }
 
 // Tiles [tile_lo, tile_hi) of an item; results to the output (more < 0: the
@@ -746,9 +746,8 @@ __device__ __forceinline__ void make_uniform(Item& j) {
 
 // One workgroup per own item.
 template <int D, int RT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, groups_per_cu(D, RT) * 4 / WAVES > 0
-                                             ? (groups_per_cu(D, RT) * 4 / WAVES) * WAVES / 4
-                                             : WAVES / 4) void attention_items(Params p) {
+__global__ __launch_bounds__(64 * WAVES, D == 64 && RT == 1 ? 4 : 2) void attention_items(
+    Params p) {
   __shared__ Shared<D, RT, WAVES> sh;
   const uint32_t block = blockIdx.x, pair = block / (uint32_t)p.kv_heads;
   Item job;
@@ -916,7 +915,16 @@ Plan plan_of(int64_t page_size, int64_t kv_heads, int64_t head_dim, int64_t batc
              int64_t groups) {
   Plan p;
   const int64_t per_seq = q_tokens * (q_heads / kv_heads);
-  p.rt = groups == 0 && per_seq <= 16 ? 1 : 2;
+  const int64_t rows_each = groups ? batch * per_seq / groups : per_seq;
+  // One row tile a workgroup, or two that share what they decode.  Two from heads of 192 on would
+  // take 416 registers and more: one workgroup per CU (16 sequences a prompt of 8192, heads of
+  // 256: 80 us with one, 116 with two).  Groups: one up to 256 rows each (4 x 64 rows x 8192 tokens
+  // 49 us with one, 51 with two; 4 x 512 rows x 16384 301 and 266).  Without groups: two where
+  // a tile would not hold a sequence's and twos are enough for all CUs (64 sequences x 64 rows x
+  // 2000 tokens 64 us with two, 80 with one; 4 such sequences 25 and 17)
+  const bool two = groups ? rows_each > 256
+                          : per_seq > 16 && batch * ceil_div(per_seq, 32) * kv_heads >= 256;
+  p.rt = head_dim <= 128 && two ? 2 : 1;
   p.blocks = ceil_div(per_seq, 16 * p.rt);
   p.rows = batch * q_tokens * q_heads;
   p.items = batch * p.blocks * kv_heads;
@@ -924,9 +932,12 @@ Plan plan_of(int64_t page_size, int64_t kv_heads, int64_t head_dim, int64_t batc
   const int64_t tokens = max_pages * page_size;
   // One workgroup per item where the contexts are short (a join costs about 5 us: 777 tokens
   // 10.4 us so, 14.3 cut) or the items so many that their unequal lengths even out.  Else as
-  // many parts as the chip holds workgroups (with a prefix: 52 us so, 60 with twice as many),
-  // twice as many where an item is one sequence's (64 x 2048-8192 tokens: 98 us, 102 with one)
-  p.parts = groups == 0 && (tokens <= 2048 || p.items >= 8 * held) ? 0 : p.rt == 1 ? 2 * held : held;
+  // many parts as the chip holds workgroups; twice as many where one tile holds a sequence's rows
+  // (64 x 2048-8192 tokens: 98 us, 102 with one); two a CU with groups, whose rows are many to
+  // join (512 rows x 16384 tokens 104 us, 128 with one, 106 with twice as many)
+  p.parts = groups ? 512
+            : tokens <= 2048 || p.items >= 8 * held ? 0
+            : per_seq <= 16 ? 2 * held : held;
   // row blocks of all groups at most, and so parts at most: each cut adds one to an item's first
   const int64_t prefix_items = groups ? (batch * per_seq / (16 * p.rt) + groups) * kv_heads : 0;
   p.groups = p.items + (p.parts ? p.parts + prefix_items : 0);
@@ -952,24 +963,18 @@ hipError_t join(const Params& p, const Plan& plan, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int D>
+template <int D, int RT>
 hipError_t launch(const Params& p, const Plan& plan, hipStream_t stream) {
+  // a row tile alone: eight wavefronts divide the tokens of an item, else four
+  constexpr int WAVES = RT == 1 ? 8 : 4;
   const uint32_t grid = (uint32_t)plan.groups;
   if (plan.parts == 0) {
-    if (plan.rt == 1)
-      attention_items<D, 1, 8><<<grid, 512, 0, stream>>>(p);
-    else
-      attention_items<D, 2, 4><<<grid, 256, 0, stream>>>(p);
+    attention_items<D, RT, WAVES><<<grid, 64 * WAVES, 0, stream>>>(p);
     return hipGetLastError();
   }
-  if (plan.rt == 1)
-    attention_parts<D, 1><<<grid, 256, 0, stream>>>(p);
-  else
-    attention_parts<D, 2><<<grid, 256, 0, stream>>>(p);
+  attention_parts<D, RT><<<grid, 256, 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (plan.rt == 1) return join<D, 1>(p, plan, stream);
-  return join<D, 2>(p, plan, stream);
+  return e != hipSuccess ? e : join<D, RT>(p, plan, stream);
 }
 
 }  // namespace
@@ -1033,10 +1038,11 @@ hipError_t kv_attention_launch(const KvCache& c, const AttentionArgs& a, hipStre
   p.parts = (int32_t)plan.parts;
   p.scale = a.scale;
   switch (c.head_dim) {
-    case 64: return launch<64>(p, plan, stream);
-    case 128: return launch<128>(p, plan, stream);
-    case 192: return launch<192>(p, plan, stream);
-    default: return launch<256>(p, plan, stream);
+    case 64: return plan.rt == 1 ? launch<64, 1>(p, plan, stream) : launch<64, 2>(p, plan, stream);
+    case 128:
+      return plan.rt == 1 ? launch<128, 1>(p, plan, stream) : launch<128, 2>(p, plan, stream);
+    case 192: return launch<192, 1>(p, plan, stream);
+    default: return launch<256, 1>(p, plan, stream);
   }
 }
 

@@ -185,6 +185,26 @@ def test_many_sequences():
           members=members).check(label="many groups")
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("max_pages", [4, 140])
+def test_many_sequences_with_many_rows(dim, max_pages):
+    # enough items that workgroups take two row tiles of 16 (up to heads of 128): 28 rows
+    # each, one of them short; whole contexts, and contexts cut into parts
+    rng = np.random.default_rng(dim)
+    lens = rng.integers(0, 65, 90)
+    lens[:4] = 0, 1, 6, 7
+    Batch(31, lens, tokens=7, heads=12, kv_heads=3, dim=dim, max_pages=max_pages).check(
+        label="%d pages" % max_pages)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192])
+def test_shared_prefix_of_many_rows(dim):
+    # groups of more than 256 rows on average, one of them small, one with an odd count
+    lens = [i % 5 for i in range(23)]
+    Batch(32, lens, tokens=3, heads=32, kv_heads=1, dim=dim, prefix_lens=[150, 333],
+          members=[0, 2, 23]).check(label="rows")
+
+
 @pytest.mark.parametrize("gain,scale", [(1.0, 0.0), (1.0, -0.3), (30.0, 1.0), (2.0 ** 60, 2.0 ** -60),
                                         (2.0 ** -70, 2.0 ** 70), (1e-3, 1.0)])
 def test_scales_of_the_scores(gain, scale):
