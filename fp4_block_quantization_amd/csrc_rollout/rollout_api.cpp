@@ -18,6 +18,9 @@ constexpr int64_t kMaxExtent = (int64_t)1 << 30;
 constexpr int64_t kMaxElements = (int64_t)1 << 40;
 constexpr int64_t kMaxGroups = 65535;
 constexpr int64_t kMaxSlots = ((int64_t)1 << 31) - 1;
+// Attention: a context's positions and a page's value scales are reached by 32-bit offsets.
+constexpr int64_t kMaxContext = (int64_t)1 << 30;
+constexpr int64_t kMaxPage = (int64_t)1 << 27;
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -53,7 +56,7 @@ fp4q_status check_cache(const fp4q::KvCache& c) {
       c.head_dim <= 0 || c.head_dim % 16 != 0 || c.head_dim > 512)
     return FP4Q_ERROR_INVALID_SHAPE;
   if (c.page_size > kMaxSlots || c.num_pages > kMaxSlots / c.page_size ||
-      c.kv_heads > kMaxExtent || !fits(c.num_pages * c.page_size, c.kv_heads * c.head_dim))
+      c.kv_heads > kMaxGroups || !fits(c.num_pages * c.page_size, c.kv_heads * c.head_dim))
     return FP4Q_ERROR_INVALID_SHAPE;
   return FP4Q_SUCCESS;
 }
@@ -88,10 +91,10 @@ bool attention_shape_ok(int64_t page_size, int64_t kv_heads, int64_t head_dim, i
       q_heads <= 0 || max_pages < 0 || max_prefix_pages < 0 || groups < 0)
     return false;
   if (head_dim != 64 && head_dim != 128 && head_dim != 192 && head_dim != 256) return false;
-  if (q_heads % kv_heads != 0 || kv_heads > 65535 || q_heads > kMaxExtent / 512) return false;
+  if (q_heads % kv_heads != 0 || kv_heads > kMaxGroups || q_heads > kMaxExtent / 512) return false;
   if (batch > kMaxGroups || groups > kMaxGroups || q_tokens > kMaxExtent) return false;
-  if (page_size > kMaxSlots || max_pages > kMaxSlots / page_size ||
-      max_prefix_pages > kMaxSlots / page_size)
+  if (page_size > kMaxPage || max_pages > kMaxContext / page_size ||
+      max_prefix_pages > kMaxContext / page_size)
     return false;
   // query rows are numbered in 31 bits
   return q_tokens == 0 || batch * q_heads <= kMaxSlots / q_tokens;

@@ -806,6 +806,8 @@ __global__ __launch_bounds__(256, groups_per_cu(D, RT)) void attention_parts(Par
   // n parts of equal length, to a tile
   const int lo = same((int)((int64_t)tiles * part / n));
   const int hi = same((int)((int64_t)tiles * (part + 1) / n));
+  // (group offsets that overlap, against the definition, could ask for more than there are)
+  if (lo > 0 && (uint32_t)(further + part - 1) >= (uint32_t)p.parts) return;
   attend<D, RT, 4>(p, job, lo, hi, further + max(part - 1, 0),
                    p.groups == 0 && n == 1 ? -1 : n - 1, sh);
 }
@@ -845,7 +847,8 @@ __global__ __launch_bounds__(256) void attention_join(Params p) {
   // r: the row's number in its item's block
   auto gather = [&](const First& first, const float* o, int r) {
     if (!ONE || lane == 0) add(first.m, first.l, o);
-    for (int i = ONE ? lane : 0; i < first.more; i += ONE ? LANES : 1) {
+    const int more = min(first.more, p.parts - first.next);
+    for (int i = ONE ? lane : 0; i < more; i += ONE ? LANES : 1) {
       const int64_t at = (int64_t)(first.next + i) * RB + r;
       const float2 ml = p.next_ml[at];
       add(ml.x, ml.y, p.next_o + at * D);

@@ -83,8 +83,8 @@ FP4Q_API int64_t mxfp4_linear_workspace_bytes(int64_t rows, int64_t n, int64_t k
  *   v_scales          uint8 [num_pages, kv_heads, head_dim/16, page_size], 4-byte aligned:
  *                     token innermost, as the value product reads them
  *   k_token_scales, v_token_scales  float [num_pages, kv_heads, page_size], 16-byte aligned
- * num_pages > 0, page_size a positive multiple of 16, kv_heads > 0, head_dim
- * a multiple of 16 up to 512; num_pages * page_size below 2^31.
+ * num_pages > 0, page_size a positive multiple of 16, kv_heads in
+ * 1 ... 65535, head_dim a multiple of 16 up to 512; num_pages * page_size below 2^31.
  */
 
 /*
@@ -136,6 +136,7 @@ FP4Q_API fp4q_status nvfp4_kv_read(const uint8_t* k_codes, const uint8_t* k_scal
  *               q_stride a multiple of 8, at least q_heads * head_dim.
  *   q_heads     a positive multiple of kv_heads; head_dim 64, 128, 192 or 256.
  *   batch, q_tokens >= 0 (nothing is launched if either is 0).
+ *   page_size   up to 2^27; max_pages and max_prefix_pages times page_size up to 2^30.
  *   page_table  int32 [batch, max_pages] on the device: page of the token
  *               o is page_table[b][o / page_size]; seq_lens int32 [batch],
  *               clamped to [0, max_pages * page_size].  Entries past a

@@ -194,3 +194,12 @@ def test_cache_shapes():
     assert c.k_codes.shape == c.v_codes.shape == (3, 2, 32, 40)
     assert c.k_scales.shape == (3, 2, 32, 5) and c.v_scales.shape == (3, 2, 5, 32)
     assert c.k_token_scales.shape == c.v_token_scales.shape == (3, 2, 32)
+
+
+def test_extents_past_the_offsets_are_rejected():
+    for f in (append, read, attend):
+        assert f(heads=65536, q_stride=1 << 25, q_heads=65536) == SHAPE
+    wide = dict(q_stride=256)
+    assert attend(pages=1, page=(1 << 27) + 16, **wide) == SHAPE
+    assert attend(max_pages=(1 << 26) + 1, **wide) == SHAPE      # more than 2^30 tokens of 16
+    assert attend(groups=1, ppages=(1 << 26) + 1, ptable=A4, plens=A4, offs=A4, **wide) == SHAPE
