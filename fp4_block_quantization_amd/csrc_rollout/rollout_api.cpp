@@ -14,6 +14,7 @@ namespace {
 // Largest sizes accepted: every element count fits in 2^40, every extent
 // that a kernel holds in an int in 2^30.
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
+constexpr int64_t kMaxDepth = (int64_t)1 << 26;  // 32 rows of weights within 32-bit offsets
 constexpr int64_t kMaxExtent = (int64_t)1 << 30;
 constexpr int64_t kMaxElements = (int64_t)1 << 40;
 constexpr int64_t kMaxGroups = 65535;
@@ -29,7 +30,7 @@ bool fits(int64_t a, int64_t b) { return b == 0 || a <= kMaxElements / b; }
 fp4q_status launched(hipError_t e) { return e == hipSuccess ? FP4Q_SUCCESS : FP4Q_ERROR_LAUNCH; }
 
 bool linear_shape_ok(int64_t rows, int64_t n, int64_t k, int64_t groups, int64_t block) {
-  return rows >= 0 && rows <= kMaxRows && n > 0 && n <= kMaxExtent && k > 0 && k <= kMaxExtent &&
+  return rows >= 0 && rows <= kMaxRows && n > 0 && n <= kMaxExtent && k > 0 && k <= kMaxDepth &&
          k % block == 0 && groups >= 0 && groups <= kMaxGroups && fits(rows, k) &&
          fits(rows, n) && fits(n, k) && (groups == 0 || fits(n * k, groups));
 }

@@ -1,8 +1,10 @@
 // rollout_linear.hip -- products with 4-bit weights and group scales
 // (definitions in include/fp4q/rollout.h).
 //
-// Both forms read every weight byte once per 16 * RT (or ROWS) rows of x
+// All forms read every weight byte once per 16 * RT (or ROWS) rows of x
 // and are bound by that read: 0.5625 bytes a weight (NVFP4), 0.53 (MXFP4).
+// 65536 x 7168 (264 MB): one row 50 us (5.3 TB/s), 16 rows 63, 64 rows 95
+// (0.63 PFLOP/s).
 //
 // One or two rows (dot form).  A wavefront takes NC output columns; a lane
 // takes 32 consecutive weights of a column at a time (16 bytes of codes, so a
@@ -288,11 +290,7 @@ __global__ __launch_bounds__(64 * WAVES) void linear_small(LinearArgs a) {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-// The scale bytes of a wavefront's 16 columns over a slab.  A step's scales
-// are two bytes a lane (NVFP4; one, MXFP4) out of 8 (4) consecutive ones of
-// each column: loaded so, four narrow loads a slab took 40% of the kernel's
-// time.  Instead lane (col, grp) loads the grp-th quarter of its column's
-// bytes in the slab at once, and the four lanes of a column exchange them.
+// A lane's scale bytes in a slab: those of its own elements, neighbours in memory.
 template <bool MX, int KS>
 struct ScaleLoad {
   static constexpr int BYTES = KS / (MX ? 32 : 16) / 4;  // 8, 4 or 2 a lane
@@ -317,41 +315,47 @@ struct ScaleLoad {
     for (int i = 0; i < BYTES; ++i)
       if (i < n) w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
   }
-  // f[s][h]: the scale of the lane's first (0) and second (1) 16 elements of step s; MXFP4's
-  // power of two, an FP32 pattern of which the conversions read the exponent field alone (so
-  // byte 0, 2^-127, works too), in f[s][0].
-  __device__ __forceinline__ void exchange(int col, int grp, float (&f)[STEPS][2]) const {
-    if constexpr (BYTES == 8) {
-      // lane group g holds, of step g, the pairs for groups 0 ... 3; a 4 x 4 transposition
-      const auto h = __builtin_amdgcn_permlane32_swap(w[0], w[1], false, false);
-      const uint32_t lo = __builtin_amdgcn_perm(h[1], h[0], 0x05040100u);
-      const uint32_t hi = __builtin_amdgcn_perm(h[1], h[0], 0x07060302u);
-      const auto r = __builtin_amdgcn_permlane16_swap(lo, hi, false, false);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {  // r[s]: the pairs of steps s and s + 2
-        f[s][0] = e4m3_value<0>(r[s]);
-        f[s][1] = e4m3_value<1>(r[s]);
-        f[s + 2][0] = e4m3_value<2>(r[s]);
-        f[s + 2][1] = e4m3_value<3>(r[s]);
-      }
-    } else if constexpr (!MX) {
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        const uint32_t e =
-            (uint32_t)__shfl((int)w[0], col + 16 * (2 * s + grp / 2)) >> (16 * (grp % 2));
-        f[s][0] = e4m3_value<0>(e);
-        f[s][1] = e4m3_value<1>(e);
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        const int from = BYTES == 4 ? s : 2 * s + grp / 2, byte = BYTES == 4 ? grp : grp % 2;
-        const uint32_t e = (uint32_t)__shfl((int)w[0], col + 16 * from) >> (8 * byte) & 255u;
-        f[s][0] = __uint_as_float(e << 23);
-      }
-    }
+  // The scale of the first (H = 0) and second 16 elements of step S; MXFP4's power of two, an
+  // FP32 pattern of which the conversions read the exponent field alone (so byte 0, 2^-127,
+  // works too), for both.
+  template <int S, int H>
+  __device__ __forceinline__ float value() const {
+    if constexpr (MX)
+      return __uint_as_float((w[S / 4] >> (8 * (S % 4)) & 255u) << 23);
+    else
+      return e4m3_value<(2 * S + H) % 4>(w[S / 2]);
   }
 };
+
+// The matrix instruction wants a column a lane, but loaded so every lane's 16 bytes are an
+// access of their own, 64 a load, and the vector memory pipe was busy for most of the time.  So N
+// neighbouring lanes read N * 16 consecutive bytes of one column, for N columns in turn, and this
+// is the transposition: w[r] of lane b of N becomes what lane r had in w[b].  (32 experts x 8 rows
+// 67 -> 61 us, 65536 x 7168 by 16 rows 71 -> 63; exchanged through LDS 63 and 64; two slabs of
+// weights ahead instead of one 62 and 65.)
+template <int N>
+__device__ __forceinline__ void turn(u32x4v (&w)[N], int lane) {
+  auto swap = [&](u32x4v& lo, u32x4v& hi, bool odd, auto from) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = lo[i], b = hi[i], fa = from(a), fb = from(b);
+      lo[i] = odd ? fb : a;
+      hi[i] = odd ? b : fa;
+    }
+  };
+  auto by_1 = [](uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true);
+  };
+  auto by_2 = [](uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true);
+  };
+#pragma unroll
+  for (int i = 0; i < N; i += 2) swap(w[i], w[i + 1], lane & 1, by_1);
+  if constexpr (N == 4) {
+    swap(w[0], w[2], lane & 2, by_2);
+    swap(w[1], w[3], lane & 2, by_2);
+  }
+}
 
 // One workgroup: 64 * NT columns (tile x0 + blockIdx.x), 16 * RT rows (block
 // y0 + blockIdx.y; with groups, all rows of that group in turn), and the
@@ -362,7 +366,10 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
                                                                      int64_t y0, float* partial) {
   constexpr int KS = RT == 1 ? 512 : 256, STEPS = KS / 128, RB = 16 * RT;
   constexpr int PIECES = KS / 8, PER_COPY = 64 / PIECES;  // 16-byte pieces a row; rows a copy
-  __shared__ alignas(16) uint8_t xs[2][RB * KS * 2];
+  // A copy's rows lie together, 1 KiB, and 16 bytes after them stay unused; the second of two
+  // rows has its pieces 8 apart exchanged: so 16 rows' reads of a piece meet all banks once.
+  constexpr int COPY = 1024 + 16;
+  __shared__ alignas(16) uint8_t xs[2][RB / PER_COPY * COPY];
   const int lane = threadIdx.x % 64, col = lane % 16, grp = lane / 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int64_t k = a.k, y = y0 + blockIdx.y;
@@ -375,19 +382,28 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
   const int slab_lo = (int)(slabs * split / splits), slab_hi = (int)(slabs * (split + 1) / splits);
   const int slab_whole = min(slab_hi, (int)(k / KS));
   const int64_t n0 = ((x0 + blockIdx.x) * 4 + wave) * 16 * NT;
-  const uint8_t* codes[NT];
+  // Lane (col, grp) multiplies the elements [grp KS/4, (grp + 1) KS/4) of a slab, 32 a step, of
+  // column n0 + 16 t + col; it loads, as w[r], the (col mod STEPS)-th 16 bytes of them of column
+  // n0 + 16 t + col - col mod STEPS + r.
+  const int first = __builtin_amdgcn_readfirstlane((int)min(n0, a.n - 1));
+  const uint8_t* codes = a.codes + (matrix * a.n + first) * (k / 2);
+  const uint32_t row_bytes = (uint32_t)(k / 2);
+  uint32_t code_at[NT][STEPS], own_at[NT];
   const uint8_t* scales[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int64_t n = matrix * a.n + min(n0 + t * 16 + col, a.n - 1);
-    codes[t] = a.codes + n * (k / 2) + grp * 16;
-    scales[t] = a.scales + n * (k / (MX ? 32 : 16)) + grp * ScaleLoad<MX, KS>::BYTES;
-  }
-  // where the lane's four 8-element pieces of a step lie in LDS: the pieces of row m are
-  // stored in the order piece ^ (m mod 16), so that 16 rows' reads meet all banks once
-  uint32_t at_piece[4];
+    auto column = [&](int c) { return (uint32_t)(min(n0 + t * 16 + c, a.n - 1) - first); };
 #pragma unroll
-  for (int q = 0; q < 4; ++q) at_piece[q] = (uint32_t)(col * KS * 2 + ((grp * 4 + q) ^ col) * 16);
+    for (int r = 0; r < STEPS; ++r)
+      code_at[t][r] = column(col / STEPS * STEPS + r) * row_bytes + grp * (KS / 8) + col % STEPS * 16;
+    own_at[t] = column(col) * row_bytes + grp * (KS / 8);
+    scales[t] = a.scales + (matrix * a.n + first + column(col)) * (k / (MX ? 32 : 16)) +
+                grp * ScaleLoad<MX, KS>::BYTES;
+  }
+  // the lane's first piece in LDS; its others follow
+  const uint32_t at_piece =
+      (uint32_t)(col / PER_COPY * COPY +
+                 (PER_COPY == 1 ? grp * 16 : col % 2 * 32 + ((grp * 8) ^ (col % 2 * 8))) * 16);
 
   for (int64_t m0 = range.first; m0 < range.last; m0 += RB) {
     const int rows = (int)min((int64_t)RB, range.last - m0);
@@ -406,12 +422,13 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
       const int64_t piece0 = (int64_t)slab * PIECES, last = k / 8 - 1;
 #pragma unroll
       for (int i = 0; i < RB / PER_COPY / 4; ++i) {
-        const int first = (i * 4 + wave) * PER_COPY;
-        if (first < rows) {
-          const int r = first + lane / PIECES;
-          const int64_t piece = min(piece0 + ((lane % PIECES) ^ (r & 15)), last);
+        const int row0 = (i * 4 + wave) * PER_COPY;
+        if (row0 < rows) {
+          const int r = row0 + lane / PIECES;
+          const int64_t piece = min(piece0 + ((lane % PIECES) ^ (lane / PIECES * 8)), last);
           __builtin_amdgcn_global_load_lds(x + (m0 + min(r, rows - 1)) * k + piece * 8,
-                                           (lds_void*)(xs[slab & 1] + first * KS * 2), 16, 0, 0);
+                                           (lds_void*)(xs[slab & 1] + row0 / PER_COPY * COPY), 16,
+                                           0, 0);
         }
       }
     };
@@ -419,15 +436,15 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
       copy(slab);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const uint8_t* c = codes[t] + (int64_t)slab * (KS / 2);
+        const uint8_t* c = codes + (int64_t)slab * (KS / 2);
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) w_next[t][s] = *(const u32x4v*)(c + s * 64);
+        for (int s = 0; s < STEPS; ++s) w_next[t][s] = *(const u32x4v*)(c + code_at[t][s]);
         e_next[t].whole(scales[t] + (int64_t)slab * (KS / (MX ? 32 : 16)));
       }
     };
-    // the slab of w, whose scales are in e_next
+    // the slab of w
     auto multiply = [&](int slab, float (&f)[NT][STEPS][2]) {
-      const uint8_t* xb = xs[slab & 1];
+      const uint8_t* xb = xs[slab & 1] + at_piece;
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
 #pragma unroll
@@ -436,7 +453,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
 #pragma unroll
           for (int r = 0; r < RT; ++r)
             if (r == 0 || r * 16 < rows)
-              xv[r] = *(const u32x4v*)(xb + at_piece[q] + r * 16 * KS * 2 + s * 256);
+              xv[r] = *(const u32x4v*)(xb + r * 16 / PER_COPY * COPY + s * 64 + q * 16);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             const bf16x8v wv = weights_of<MX>(w[t][s][q], f[t][s][MX ? 0 : q / 2]);
@@ -447,13 +464,23 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
         }
       }
     };
-    auto begin = [&](float (&f)[NT][STEPS][2]) {
+    auto begin = [&](bool turned, float (&f)[NT][STEPS][2]) {
       __builtin_amdgcn_s_waitcnt(0);  // this wavefront's copies and weights have landed
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) w[t][s] = w_next[t][s];
-        e_next[t].exchange(col, grp, f[t]);
+        if (!turned) turn<STEPS>(w[t], lane);
+        f[t][0][0] = e_next[t].template value<0, 0>();
+        f[t][0][1] = e_next[t].template value<0, 1>();
+        f[t][1][0] = e_next[t].template value<1, 0>();
+        f[t][1][1] = e_next[t].template value<1, 1>();
+        if constexpr (STEPS == 4) {
+          f[t][2][0] = e_next[t].template value<2, 0>();
+          f[t][2][1] = e_next[t].template value<2, 1>();
+          f[t][3][0] = e_next[t].template value<3, 0>();
+          f[t][3][1] = e_next[t].template value<3, 1>();
+        }
       }
       __syncthreads();  // the other wavefronts' copies too; the slab before is read
     };
@@ -462,7 +489,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
     if (slab_lo < slab_whole) load(slab_lo);
     for (int slab = slab_lo; slab < slab_whole; ++slab) {
       float f[NT][STEPS][2];
-      begin(f);
+      begin(false, f);
       if (slab + 1 < slab_whole) load(slab + 1);
       multiply(slab, f);
     }
@@ -471,15 +498,15 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
       copy(slab_whole);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const uint8_t* c = codes[t] + (int64_t)slab_whole * (KS / 2);
+        const uint8_t* c = codes + (int64_t)slab_whole * (KS / 2) + own_at[t];
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-          const int at = s * 128 + grp * 32;
+          const int at = grp * (KS / 4) + s * 32;
           w_next[t][s] = (u32x4v){0, 0, 0, 0};
           if (at + 32 <= left) {
-            w_next[t][s] = *(const u32x4v*)(c + s * 64);
+            w_next[t][s] = *(const u32x4v*)(c + s * 16);
           } else if (!MX && at + 16 <= left) {
-            const u32x2v half = *(const u32x2v*)(c + s * 64);
+            const u32x2v half = *(const u32x2v*)(c + s * 16);
             w_next[t][s] = (u32x4v){half[0], half[1], 0, 0};
           }
         }
@@ -487,7 +514,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
                        left / (MX ? 32 : 16) - grp * ScaleLoad<MX, KS>::BYTES);
       }
       float f[NT][STEPS][2];
-      begin(f);
+      begin(true, f);
       multiply(slab_whole, f);
     }
 

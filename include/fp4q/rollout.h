@@ -36,7 +36,7 @@ extern "C" {
  *   codes         uint8 [n, k/2] ([num_groups, n, k/2] with groups), 8-byte
  *                 aligned; block_scales uint8 [.., n, k/16] (E4M3FN);
  *                 row_scales float [.., n], 4-byte aligned.
- *   rows          >= 0 (0: nothing is launched); n > 0; k > 0, a multiple of 16.
+ *   rows          >= 0 (0: nothing is launched); n > 0; k > 0, a multiple of 16, up to 2^26.
  *   group_offsets NULL, or int64 [num_groups + 1] on the device, 8-byte
  *                 aligned, non-decreasing, within [0, rows]: the rows
  *                 [off[e], off[e+1]) are multiplied with expert e's matrix;
@@ -63,7 +63,7 @@ FP4Q_API int64_t nvfp4_linear_workspace_bytes(int64_t rows, int64_t n, int64_t k
  * scales of mxfp4_resq_quantize): w = +-g(code) * 2^(byte - 127).
  *
  *   codes   uint8 [.., n, k/2], 16-byte aligned; scales uint8 [.., n, k/32] (E8M0).
- *   k       a multiple of 32.  Everything else: as for nvfp4_linear.
+ *   k       a multiple of 32, up to 2^26.  Everything else: as for nvfp4_linear.
  */
 FP4Q_API fp4q_status mxfp4_linear(const void* x, int64_t rows, const uint8_t* codes,
                                   const uint8_t* scales, int64_t n, int64_t k,

@@ -147,3 +147,28 @@ def test_cache_past_four_gib():
     for got, src in zip(results[1], (k, v)):
         want = fq.nvfp4_quantize(src.reshape(-1, dim), dequant=True)[3]
         assert torch.equal(got.reshape(-1, dim).view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("rows,grouped", [(1, False), (5, False), (20, False), (40, True)])
+def test_longest_rows(rows, grouped, mx):
+    # k at its limit: only the last elements of x are not zero
+    k, n, used = 2 ** 26, 40, 4096 + 96
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    codes = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    scales = torch.full((n, k // (32 if mx else 16)), 120 if mx else 0x35, dtype=torch.uint8,
+                        device="cuda")
+    x_bits = workloads.random_rows(rows, rows, used, dist=1)
+    x = torch.zeros((rows, k), dtype=torch.bfloat16, device="cuda")
+    x[:, -used:] = to_dev(x_bits)
+    q = [codes, scales] if mx else [codes, scales, torch.ones(n, device="cuda")]
+    tail = [codes[:, -used // 2:].cpu().numpy(), scales[:, -used // (32 if mx else 16):].cpu().numpy()]
+    w = ru.mx_values(*tail) if mx else ru.nv_values(*tail, np.ones(n))
+    offsets = None
+    if grouped:
+        q = [t[None] for t in q]
+        offsets = torch.tensor([0, rows], device="cuda")
+    linear = fq.mxfp4_linear if mx else fq.nvfp4_linear
+    y = linear(x, *q, offsets=offsets, out_dtype=torch.float32)
+    want, bound = ru.linear_bound(ru.bf16_values(x_bits), w, False)
+    ru.check(y.cpu().numpy(), want, bound, "k=2^26")

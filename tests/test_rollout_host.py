@@ -203,3 +203,5 @@ def test_extents_past_the_offsets_are_rejected():
     assert attend(pages=1, page=(1 << 27) + 16, **wide) == SHAPE
     assert attend(max_pages=(1 << 26) + 1, **wide) == SHAPE      # more than 2^30 tokens of 16
     assert attend(groups=1, ppages=(1 << 26) + 1, ptable=A4, plens=A4, offs=A4, **wide) == SHAPE
+    for mx in (False, True):
+        assert linear(mx=mx, rows=1, n=1, k=(1 << 26) + 32) == SHAPE
