@@ -10,8 +10,10 @@
 //
 // One lane per 16-element block, a row's blocks in neighbouring lanes: a
 // wavefront reads (or writes) 2 KiB of consecutive BF16, and whole rows of
-// codes.  Reading is bound by memory; writing about equally by the two
-// candidates' arithmetic, some 18 vector instructions an element.
+// codes.  Reading is bound by memory: 32k tokens of 8 heads of 128 take 30
+// us, 5.6 TB/s.  Writing is bound about equally by memory and the two
+// candidates' arithmetic, some 18 vector instructions an element: 8k such
+// tokens take 13.3 us, 3.2 TB/s.
 #include "fp4q_device.h"
 #include "rollout_divisor.h"
 #include "rollout_launch.h"
