@@ -11,9 +11,10 @@
 // One lane per 16-element block, a row's blocks in neighbouring lanes: a
 // wavefront reads (or writes) 2 KiB of consecutive BF16, and whole rows of
 // codes.  Reading is bound by memory: 32k tokens of 8 heads of 128 take 30
-// us, 5.6 TB/s.  Writing is bound about equally by memory and the two
-// candidates' arithmetic, some 18 vector instructions an element: 8k such
-// tokens take 13.3 us, 3.2 TB/s.
+// us, 5.6 TB/s.  8k such tokens are written in 12.4 us, 3.5 TB/s (13.3 with
+// the errors of every block by the definition): memory takes 7 of them, the
+// rest are the launch, loads behind loads in wavefronts that do one block a
+// lane, and the value scales' single bytes (1 us).
 #include "fp4q_device.h"
 #include "rollout_divisor.h"
 #include "rollout_launch.h"
@@ -59,18 +60,83 @@ __device__ __forceinline__ Place place_of(const CacheView& c, uint32_t slot, uin
   return p;
 }
 
-// One candidate of a block: its scale byte, codes and squared error.
+// One candidate of a block: its scale byte, codes and squared error; of a
+// row with 2^-50 <= s <= 2^40 first only a, the error in units of the decode
+// step d = e s, and d^2.
 struct Candidate {
   uint32_t e_byte;
   uint32_t word[2];
-  float err;
+  float err, a, d2;
 };
+
+// The scale byte of one candidate.  A zero row (s = 0) has zero scales; the quotient rounds to
+// at most 448.
+__device__ __forceinline__ uint32_t scale_byte(float b, float s, float k) {
+  const float t = s > 0.0f ? fminf(b / (k * s), 448.0f) : 0.0f;
+  return cvt_e4m3x2(t, t) & 0xFFu;
+}
+
+__device__ __forceinline__ void encode(const float* x, float b, float s, float k, Candidate& c) {
+  c.e_byte = scale_byte(b, s, k);
+  const float d = e4m3_value<0>(c.e_byte) * s;
+  const float r = d == 0.0f ? 0.0f : recip_normal(d);
+  c.a = 0.0f;
+  c.d2 = d * d;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = x[8 * w + i] * r;
+    uint32_t q = cvt_e2m1x2<0>(any_word(), v[0], v[1]);
+    q = cvt_e2m1x2<1>(q, v[2], v[3]);
+    q = cvt_e2m1x2<2>(q, v[4], v[5]);
+    q = cvt_e2m1x2<3>(q, v[6], v[7]);
+    c.word[w] = q;
+    const float2v g[4] = {e2m1x2_values<0>(q), e2m1x2_values<1>(q), e2m1x2_values<2>(q),
+                          e2m1x2_values<3>(q)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float diff = v[i] - g[i / 2][i % 2];
+      c.a = __builtin_fmaf(diff, diff, c.a);
+    }
+  }
+}
+
+// The definition's squared error of a candidate's codes.
+__device__ __forceinline__ float error_of(const float* x, const Candidate& c, float s) {
+  const float e = e4m3_value<0>(c.e_byte);
+  float err = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const uint32_t q = c.word[w];
+    const float2v g[4] = {e2m1x2_values<0>(q), e2m1x2_values<1>(q), e2m1x2_values<2>(q),
+                          e2m1x2_values<3>(q)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float diff = x[8 * w + i] - (g[i / 2][i % 2] * e) * s;
+      err = err + diff * diff;
+    }
+  }
+  return err;
+}
+
+// Whether the candidate for 4 has the lower error, as far as a and d^2 tell.  With u = 2^-24,
+// |v| < 10 and |g| <= 6, each x - c of the definition is within 32.2 u d of d (v - g), and its
+// sum of squares, summed in FP32, within d^2 (163.4 u a + 129.3 u) of d^2 a (nvfp4_quantize's
+// kernel derives it); the differences, sums and margin below are within 2.1 u of theirs.  So
+// twice that margin decides, and what it leaves open the errors by the definition do.
+__device__ __forceinline__ bool four_is_lower(const Candidate& six, const Candidate& four,
+                                              bool& sure) {
+  constexpr float u = 0x1p-24f;
+  const float p = four.d2 * four.a, q = six.d2 * six.a, diff = q - p;
+  const float margin = __builtin_fmaf(p + q, 330.0f * u, (four.d2 + six.d2) * (260.0f * u));
+  sure = __builtin_fabsf(diff) > margin && six.e_byte != 0;
+  return diff > margin;
+}
 
 __device__ __forceinline__ Candidate candidate(const float* x, float b, float s, float k) {
   Candidate c;
-  // a zero row (s = 0) has zero scales; the quotient rounds to at most 448
-  const float t = s > 0.0f ? fminf(b / (k * s), 448.0f) : 0.0f;
-  c.e_byte = cvt_e4m3x2(t, t) & 0xFFu;
+  c.e_byte = scale_byte(b, s, k);
   const float e = e4m3_value<0>(c.e_byte), d = e * s;
   c.err = 0.0f;
   if (d >= 0x1p-126f || d == 0.0f) {
@@ -143,10 +209,22 @@ __global__ __launch_bounds__(256) void kv_append_kernel(CacheView c, const uint1
 #pragma unroll
   for (int step = LANES / 2; step > 0; step >>= 1) amax = fmaxf(amax, __shfl_xor(amax, step));
   const float s = amax_over_c(amax, fos != 0);
-  Candidate q = candidate(x, b, s, 6.0f);
-  if (fos) {
-    const Candidate q4 = candidate(x, b, s, 4.0f);
-    if (q4.err < q.err) q = q4;
+  Candidate q;
+  if (__all(s >= 0x1p-50f && s <= 0x1p40f)) {
+    encode(x, b, s, 6.0f, q);
+    if (fos) {
+      Candidate q4;
+      encode(x, b, s, 4.0f, q4);
+      bool sure, four = four_is_lower(q, q4, sure);
+      if (!sure) four = error_of(x, q4, s) < error_of(x, q, s);
+      if (four) q = q4;
+    }
+  } else {
+    q = candidate(x, b, s, 6.0f);
+    if (fos) {
+      const Candidate q4 = candidate(x, b, s, 4.0f);
+      if (q4.err < q.err) q = q4;
+    }
   }
   if (!live || slot < 0 || slot >= c.slots) return;
   const Place p = place_of(c, (uint32_t)slot, head, block, which);
