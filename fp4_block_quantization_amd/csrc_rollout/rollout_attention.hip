@@ -945,7 +945,8 @@ Plan plan_of(int64_t page_size, int64_t kv_heads, int64_t head_dim, int64_t batc
   // 10.4 us so, 14.3 cut) or the items so many that their unequal lengths even out.  Else as
   // many parts as the chip holds workgroups; twice as many where one tile holds a sequence's rows
   // (64 x 2048-8192 tokens: 98 us, 102 with one); two a CU with groups, whose rows are many to
-  // join (512 rows x 16384 tokens 104 us, 128 with one, 106 with twice as many)
+  // join (4 x 256 rows x 8192 tokens 61 us, 72 with one a CU, 61 with three; 4 x 64 rows 49, 46
+  // and 49; the same with heads of 64 33, 36 and 36)
   p.parts = groups ? 512
             : tokens <= 2048 || p.items >= 8 * held ? 0
             : per_seq <= 16 ? 2 * held : held;
