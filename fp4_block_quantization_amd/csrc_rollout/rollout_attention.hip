@@ -855,7 +855,9 @@ __global__ __launch_bounds__(256) void attention_join(Params p) {
   // r: the row's number in its item's block
   auto gather = [&](const First& first, const float* o, int r) {
     if (!ONE || lane == 0) add(first.m, first.l, o);
-    const int more = min(first.more, p.parts - first.next);
+    // (within the workspace, whatever overlapping groups have left unwritten)
+    const int more =
+        (uint32_t)first.next < (uint32_t)p.parts ? min(first.more, p.parts - first.next) : 0;
     for (int i = ONE ? lane : 0; i < more; i += ONE ? LANES : 1) {
       const int64_t at = (int64_t)(first.next + i) * RB + r;
       const float2 ml = p.next_ml[at];
