@@ -843,8 +843,7 @@ __global__ __launch_bounds__(256) void attention_join(Params p) {
 
   float top = -INFINITY, total = 0.0f;
   float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  auto add = [&](float m, float l, const float* o) {
-    const float4v v = *(const float4v*)(o + d);
+  auto add = [&](float m, float l, float4v v) {
     const float grown = m > top ? m : top;  // a NaN in l and O stays one in the sums
     const float base = grown == -INFINITY ? 0.0f : grown;
     const float keep = factor(top, base), f = factor(m, base);
@@ -854,15 +853,28 @@ __global__ __launch_bounds__(256) void attention_join(Params p) {
   };
   // r: the row's number in its item's block
   auto gather = [&](const First& first, const float* o, int r) {
-    if (!ONE || lane == 0) add(first.m, first.l, o);
+    const float4v v = *(const float4v*)(o + d);
     // (within the workspace, whatever overlapping groups have left unwritten)
     const int more =
         (uint32_t)first.next < (uint32_t)p.parts ? min(first.more, p.parts - first.next) : 0;
-    for (int i = ONE ? lane : 0; i < more; i += ONE ? LANES : 1) {
-      const int64_t at = (int64_t)(first.next + i) * RB + r;
-      const float2 ml = p.next_ml[at];
-      add(ml.x, ml.y, p.next_o + at * D);
+    // some parts at a time, so that their loads are in flight together (one context of 32k
+    // tokens 21.1 -> 19.7 us)
+    constexpr int STEP = ONE ? LANES : 1, MANY = 4;
+    for (int i = ONE ? lane : 0; i < more; i += STEP * MANY) {
+      float2 ml[MANY];
+      float4v part[MANY];
+#pragma unroll
+      for (int j = 0; j < MANY; ++j) {
+        const int64_t at = (int64_t)(first.next + min(i + j * STEP, more - 1)) * RB + r;
+        ml[j] = p.next_ml[at];
+        part[j] = *(const float4v*)(p.next_o + at * D + d);
+      }
+      if (i == 0) add(first.m, first.l, v);
+#pragma unroll
+      for (int j = 0; j < MANY; ++j)
+        if (i + j * STEP < more) add(ml[j].x, ml[j].y, part[j]);
     }
+    if (more <= 0 && (!ONE || lane == 0)) add(first.m, first.l, v);
   };
   if (p.groups > 0) {
     // the last group that starts at or before this row's sequence
