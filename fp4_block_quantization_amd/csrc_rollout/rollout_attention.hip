@@ -754,8 +754,9 @@ __device__ __forceinline__ void make_uniform(Item& j) {
 
 // One workgroup per own item.
 template <int D, int RT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, D == 64 && RT == 1 ? 4 : 2) void attention_items(
-    Params p) {
+__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? groups_per_cu(D, RT)
+                                         : D == 64  ? 4
+                                                    : 2) void attention_items(Params p) {
   __shared__ Shared<D, RT, WAVES> sh;
   const uint32_t block = blockIdx.x, pair = block / (uint32_t)p.kv_heads;
   Item job;
@@ -927,6 +928,7 @@ __global__ __launch_bounds__(256) void attention_join(Params p) {
 
 struct Plan {
   int rt;  // 16-row tiles of queries per wavefront
+  bool wide;  // items: eight wavefronts a workgroup, not four
   int64_t blocks, items, rows;
   int64_t parts;   // 0: one workgroup per item
   int64_t groups;  // workgroups
@@ -955,14 +957,19 @@ Plan plan_of(int64_t page_size, int64_t kv_heads, int64_t head_dim, int64_t batc
   p.items = batch * p.blocks * kv_heads;
   const int64_t held = 256 * groups_per_cu((int)head_dim, p.rt);
   const int64_t tokens = max_pages * page_size;
+  // One row tile: eight wavefronts a workgroup where the chip holds all of them at once (128
+  // items of heads of 128, up to 700 tokens: 9.3 us with eight, 10.9 with four), else four
+  // (512 items of 512 tokens 19.8 and 13.8, 2048 of 30-500 58 and 32)
+  p.wide = p.rt == 1 && p.items <= (head_dim == 64 ? 512 : 256);
   // One workgroup per item where the contexts are short (a join costs about 5 us: 777 tokens
-  // 10.4 us so, 14.3 cut) or the items so many that their unequal lengths even out.  Else as
-  // many parts as the chip holds workgroups; twice as many where one tile holds a sequence's rows
-  // (64 x 2048-8192 tokens: 98 us, 102 with one); two a CU with groups, whose rows are many to
-  // join (4 x 256 rows x 8192 tokens 61 us, 72 with one a CU, 61 with three; 4 x 64 rows 49, 46
+  // 10.4 us so, 14.3 cut), also longer ones where items keep all CUs busy (512 of 2000-4000
+  // tokens 54 and 64; but one of 3900 among 300s 34 and 21), or the items so many that their
+  // unequal lengths even out.  Else as many parts as the chip holds workgroups; twice as many
+  // where one tile holds a sequence's rows (64 x 2048-8192 tokens: 98 us, 102 with one); two a CU
+  // with groups, whose rows are many to join (4 x 256 rows x 8192 tokens 61 us, 72 with one a CU, 61 with three; 4 x 64 rows 49, 46
   // and 49; the same with heads of 64 33, 36 and 36)
   p.parts = groups ? 512
-            : tokens <= 2048 || p.items >= 8 * held ? 0
+            : tokens <= (p.items > 256 ? 4096 : 2048) || p.items >= 8 * held ? 0
             : per_seq <= 16 ? 2 * held : held;
   // row blocks of all groups at most, and so parts at most: each cut adds one to an item's first
   const int64_t prefix_items = groups ? (batch * per_seq / (16 * p.rt) + groups) * kv_heads : 0;
@@ -991,11 +998,15 @@ hipError_t join(const Params& p, const Plan& plan, hipStream_t stream) {
 
 template <int D, int RT>
 hipError_t launch(const Params& p, const Plan& plan, hipStream_t stream) {
-  // a row tile alone: eight wavefronts divide the tokens of an item, else four
-  constexpr int WAVES = RT == 1 ? 8 : 4;
   const uint32_t grid = (uint32_t)plan.groups;
   if (plan.parts == 0) {
-    attention_items<D, RT, WAVES><<<grid, 64 * WAVES, 0, stream>>>(p);
+    if constexpr (RT == 1) {
+      if (plan.wide) {
+        attention_items<D, RT, 8><<<grid, 512, 0, stream>>>(p);
+        return hipGetLastError();
+      }
+    }
+    attention_items<D, RT, 4><<<grid, 256, 0, stream>>>(p);
     return hipGetLastError();
   }
   attention_parts<D, RT><<<grid, 256, 0, stream>>>(p);

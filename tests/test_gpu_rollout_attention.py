@@ -197,6 +197,27 @@ def test_many_sequences_with_many_rows(dim, max_pages):
         label="%d pages" % max_pages)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+def test_many_short_contexts(dim):
+    # more items than eight wavefronts each would fill the chip with at once
+    rng = np.random.default_rng(dim + 1)
+    lens = rng.integers(0, 300, 90)
+    lens[:5] = 0, 1, 63, 64, 65
+    Batch(33, lens, heads=12, kv_heads=6, dim=dim).check(label="many short")
+
+
+@pytest.mark.parametrize("tokens", [1, 7])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_many_sequences_in_parts(dim, tokens):
+    # many items whose tables have room for more than 4096 tokens: contexts cut into parts, one
+    # row tile or two, the part found by all threads of a workgroup
+    rng = np.random.default_rng(dim + tokens)
+    lens = rng.integers(0, 200, 90)
+    lens[:5] = 0, 1, 6, 1300, 64
+    Batch(34, lens, tokens=tokens, heads=12, kv_heads=3, dim=dim, max_pages=260).check(
+        label="in parts")
+
+
 @pytest.mark.parametrize("dim", [64, 128, 192])
 def test_shared_prefix_of_many_rows(dim):
     # groups of more than 256 rows on average, one of them small, one with an odd count
