@@ -36,12 +36,13 @@
 // joins the parts of an item in a fixed order.
 //
 // What bounds it.  Long contexts: the cache's bytes.  64 sequences of 64
-// heads over 8 of 128, 2048 to 8192 tokens each (400 MB), take 97 us, 4.1
+// heads over 8 of 128, 2048 to 8192 tokens each (400 MB), take 95 us, 4.2
 // TB/s; the longer the contexts the nearer to 88% of a copy's rate, as some
 // 18 us are the launch, the first loads (table, then tokens), the last parts
 // and the join.  Prompts shared by 16 sequences: decoding, repeated for each
-// 16 rows (49 us; one read of the bytes would take 12).  Small batches: the
-// chain of dependent loads, about 10 us.
+// 16 rows (48 us; one read of the bytes would take 12).  Small batches: 4 us
+// without any token, and 3 for each of a wavefront's steps, whose chain of
+// scores, softmax and values few wavefronts do not cover (777 tokens 10.5).
 #include "fp4q_device.h"
 #include "rollout_divisor.h"
 #include "rollout_launch.h"
@@ -963,13 +964,14 @@ Plan plan_of(int64_t page_size, int64_t kv_heads, int64_t head_dim, int64_t batc
   p.wide = p.rt == 1 && p.items <= (head_dim == 64 ? 512 : 256);
   // One workgroup per item where the contexts are short (a join costs about 5 us: 777 tokens
   // 10.4 us so, 14.3 cut), also longer ones where items keep all CUs busy (512 of 2000-4000
-  // tokens 54 and 64; but one of 3900 among 300s 34 and 21), or the items so many that their
+  // tokens 54 and 64, 256 of 1000-4000 29 and 37, 64 of 2000-4000 26 and 19; but one of 3900
+  // among 300s 34 and 21), or the items so many that their
   // unequal lengths even out.  Else as many parts as the chip holds workgroups; twice as many
   // where one tile holds a sequence's rows (64 x 2048-8192 tokens: 98 us, 102 with one); two a CU
-  // with groups, whose rows are many to join (4 x 256 rows x 8192 tokens 61 us, 72 with one a CU, 61 with three; 4 x 64 rows 49, 46
-  // and 49; the same with heads of 64 33, 36 and 36)
+  // with groups, whose rows are many to join (4 x 256 rows x 8192 tokens 61 us, 72 with one a CU,
+  // 61 with three; 4 x 64 rows 49, 46 and 49; the same with heads of 64 33, 36 and 36)
   p.parts = groups ? 512
-            : tokens <= (p.items > 256 ? 4096 : 2048) || p.items >= 8 * held ? 0
+            : tokens <= (p.items >= 256 ? 4096 : 2048) || p.items >= 8 * held ? 0
             : per_seq <= 16 ? 2 * held : held;
   // row blocks of all groups at most, and so parts at most: each cut adds one to an item's first
   const int64_t prefix_items = groups ? (batch * per_seq / (16 * p.rt) + groups) * kv_heads : 0;
