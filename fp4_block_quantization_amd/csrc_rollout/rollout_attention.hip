@@ -493,6 +493,16 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
   }
   half8v q[RT][NK];
   float c_q[RT];
+  // The score factor of a row, scale log2(e) 2^-ex, leaves FP32's range where tiny queries meet
+  // a small scale, or huge ones a large one.  Then it is held times 2^lift, and the token scales
+  // divided by that, with the lift that brings the largest factor of the wavefront's rows to
+  // [0.5, 1): the others are smaller as their queries are.  (Ordinary rows, whose factors lie
+  // around 2^-16, keep 0: without the reduction over the rows, which takes 0.2 us.)
+  const float factor_part = __builtin_amdgcn_frexp_mantf(__builtin_fabsf(p.scale) * kLog2e);
+  const int factor_exp = __builtin_amdgcn_frexp_expf(__builtin_fabsf(p.scale) * kLog2e);
+  constexpr int kNone = -100000;
+  int c_exp[RT], lift = 0;
+  bool far = false;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     uint32_t top = 0;
@@ -508,9 +518,8 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
     const int field = (int)(top >> 7);
     const int ex = top == 0 || field == 255 ? 0 : 14 + 127 - max(field, 1);
     const float sign = p.scale < 0.0f ? -1.0f : 1.0f;
-    // (never 0, so that a masked score's -infinity stays one)
-    c_q[rt] = p.scale == 0.0f ? 0x1p-149f
-                              : __builtin_ldexpf(__builtin_fabsf(p.scale) * kLog2e, -ex);
+    c_exp[rt] = top == 0 || p.scale == 0.0f ? kNone : factor_exp - ex;
+    far |= c_exp[rt] != kNone && (c_exp[rt] < -32 || c_exp[rt] > 64);
 #pragma unroll
     for (int k = 0; k < NK; ++k)
 #pragma unroll
@@ -519,6 +528,18 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
         q[rt][k][2 * i + 1] = (_Float16)__builtin_ldexpf(bf16_hi(raw[rt][k][i]) * sign, ex);
       }
   }
+  if (__any(far)) {
+    int most = kNone;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) most = max(most, c_exp[rt]);
+#pragma unroll
+    for (int s = 8; s > 0; s /= 2) most = max(most, __shfl_xor(most, s));
+    lift = -most;
+  }
+  // (never 0, so that a masked score's -infinity stays one)
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+    c_q[rt] = fmaxf(__builtin_ldexpf(factor_part, c_exp[rt] + lift), 0x1p-149f);
   for (int step = 0; step < steps; ++step) {
     const int t0 = (tile_lo + wave + step * WAVES) * kTile;
     const int left = job.len - t0;  // tokens of this tile that exist
@@ -562,7 +583,7 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) o[rt][dt] *= shrink;
     }
-    tile.k_scale[lane] = kt;
+    tile.k_scale[lane] = __builtin_ldexpf(kt, -lift);
     tile.v_scale[lane] = vt_live * norm;
     if ((step + 1) % 16 == 0) load_pages(step + 1);
     locate(step + 1);
