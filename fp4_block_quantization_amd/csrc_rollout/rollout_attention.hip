@@ -7,7 +7,7 @@
 // 2688), so the matrix units take them as they are:
 //   S[t][q] = sum_d (g e)[t][d] q[d]       q scaled by a power of two into
 //                                          FP16's range, exactly
-//   x = S s_t c_q                          c_q: scale, log2(e), q's power of two
+//   x = (S (s_t f)) c_q                    scale log2(e) = f 2^n; c_q: 2^n, q's power of two
 //   p = 2^(x - m), l += p, m the running maximum of x
 //   O[d][q] += sum_t (g' e')[t][d] w,  w = FP16(p s'_t / b)
 // with b a power of two at or above every s'_t met so far times 2^-15: token
@@ -497,7 +497,9 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
   // a small scale, or huge ones a large one.  Then it is held times 2^lift, and the token scales
   // divided by that, with the lift that brings the largest factor of the wavefront's rows to
   // [0.5, 1): the others are smaller as their queries are.  (Ordinary rows, whose factors lie
-  // around 2^-16, keep 0: without the reduction over the rows, which takes 0.2 us.)
+  // around 2^-16, keep 0: without the reduction over the rows, which takes 0.2 us.)  The factor's
+  // mantissa, the same for all rows, goes with the token scales, so that c_q is a power of two:
+  // its products are exact, and so is their difference to m, however large the scores are.
   const float factor_part = __builtin_amdgcn_frexp_mantf(__builtin_fabsf(p.scale) * kLog2e);
   const int factor_exp = __builtin_amdgcn_frexp_expf(__builtin_fabsf(p.scale) * kLog2e);
   constexpr int kNone = -100000;
@@ -539,7 +541,7 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
   // (never 0, so that a masked score's -infinity stays one)
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
-    c_q[rt] = fmaxf(__builtin_ldexpf(factor_part, c_exp[rt] + lift), 0x1p-149f);
+    c_q[rt] = fmaxf(__builtin_ldexpf(1.0f, c_exp[rt] + lift), 0x1p-149f);
   for (int step = 0; step < steps; ++step) {
     const int t0 = (tile_lo + wave + step * WAVES) * kTile;
     const int left = job.len - t0;  // tokens of this tile that exist
@@ -583,7 +585,7 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) o[rt][dt] *= shrink;
     }
-    tile.k_scale[lane] = __builtin_ldexpf(kt, -lift);
+    tile.k_scale[lane] = __builtin_ldexpf(kt * factor_part, -lift);
     tile.v_scale[lane] = vt_live * norm;
     if ((step + 1) % 16 == 0) load_pages(step + 1);
     locate(step + 1);

@@ -1,6 +1,7 @@
 """nvfp4_kv_attention where scores leave the ordinary range: score factors
-and queries so small that their product leaves FP32, and keys and queries
-whose magnitudes make up for each other."""
+and queries so small that their product leaves FP32, keys and queries whose
+magnitudes make up for each other, and scores whose spacing in FP32 is more
+than one."""
 import numpy as np
 import pytest
 import torch
@@ -63,3 +64,44 @@ def test_queries_far_apart():
         b.q_bits[:, :, h] = scaled_bits(b.q_bits[:, :, h].reshape(-1, 128),
                                         2.0 ** (20 - 130 * h // 7)).reshape(len(LENS), 1, 128)
     b.check(scale=2.0 ** -20, label="apart")
+
+
+@pytest.mark.parametrize("tokens", [1, 2])
+@pytest.mark.parametrize("scale", [2.0 ** 18, 2.0 ** 30, -2.0 ** 45, 2.0 ** 100])
+def test_scores_far_beyond_one(scale, tokens):
+    # FP32 tells such scores apart by more than one: only the largest has any weight.  Keys of
+    # small whole numbers have products that are exact, whatever is summed first
+    b = Batch(44, LENS, tokens=tokens, heads=4, kv_heads=2, dim=64)
+    rng = np.random.default_rng(3)
+    slots = np.concatenate([b._slots(b.table[i], n) for i, n in enumerate(b.lens)]).astype(np.int64)
+    k = rng.integers(-3, 4, (len(slots), 2, 64)).astype(np.float32)
+    k[:, :, ::16] = 6.0  # every block's scale is one, or two thirds
+    v = workloads.random_rows(5, len(slots) * 2, 64)
+    fq.nvfp4_kv_append(b.cache, torch.from_numpy(k).bfloat16().cuda(),
+                       to_dev(v).view(len(slots), 2, 64), torch.from_numpy(slots).cuda(),
+                       four_over_six=False)
+    q = rng.integers(-2, 3, b.q_bits.shape).astype(np.float32)
+    b.q_bits = workloads.to_bf16_bits(q.reshape(-1, 64)).reshape(b.q_bits.shape)
+    got, lse = b.run(scale=scale, lse=True)
+    got, lse = got.float().cpu().numpy(), lse.cpu().numpy()
+    b.host = [t.cpu().numpy() for t in b.cache]
+    for i, n in enumerate(b.lens):
+        kk, vv = b._values(b.table[i], n)
+        for t in range(tokens):
+            m = max(0, n - tokens + 1 + t)
+            for h in range(4):
+                where = "sequence %d query %d head %d" % (i, t, h)
+                if m == 0:
+                    assert not got[i, t, h].any() and np.isneginf(lse[i, t, h]), where
+                    continue
+                s = (kk[:m, h // 2] @ q[i, t, h].astype(np.float64)) * np.sign(scale)
+                # the token scale's own rounding may order equal products: leave near ties out
+                order = np.sort(s)
+                near = s >= order[-1] - 2.0 ** -18 * np.abs(s).max()
+                assert np.isfinite(got[i, t, h]).all() and np.isfinite(lse[i, t, h]), where
+                np.testing.assert_allclose(lse[i, t, h], order[-1] * abs(scale), rtol=2.0 ** -17,
+                                           atol=1.0, err_msg=where)
+                if near.sum() == 1:
+                    want = vv[np.argmax(s), h // 2]
+                    assert (np.abs(got[i, t, h] - want)
+                            <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * np.abs(vv).max()).all(), where
