@@ -10,11 +10,14 @@
 //   x = (S (s_t f)) c_q                    scale log2(e) = f 2^n; c_q: 2^n, q's power of two
 //   p = 2^(x - m), l += p, m the running maximum of x
 //   O[d][q] += sum_t (g' e')[t][d] w,  w = FP16(p s'_t / b)
-// with b a power of two at or above every s'_t met so far times 2^-15: token
-// scales differ by orders of magnitude, and w keeps FP16's full precision
-// over 29 binades below the largest (probabilities are rounded to 11 bits;
-// BF16, with 8, is what the output holds).  The scales s and s' cost one
-// multiplication per score instead of one per element.
+// with b a power of two at or above every s'_t met so far times 2^-14.  Where
+// token scales are within 2^14 of each other, w keeps 11 bits for every token
+// whose p s' is within 2^12 of the row's largest, and an error of 2^-23 of that
+// below (the output holds 8 bits).  Where they lie further apart, large ones
+// may have no weight in a row: then m is lowered row by row until its largest
+// w is near 2^14.  The scales s and s' cost one multiplication per score
+// instead of one per element.  FP16 queries lose what is below 2^-39 of their
+// row's largest element, and bits from 2^-29 on.
 //
 // Layout.  S is computed transposed (keys as rows of the 16x16x32 matrix
 // instruction, queries as columns): a lane then holds, for one query, four
@@ -58,6 +61,7 @@ typedef int int2v __attribute__((ext_vector_type(2)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr int kTile = 64;  // tokens per step of a wavefront
+constexpr float kFar = 0x1p14f;  // ratio of value scales from which they count as far apart
 
 // Beside the sums of a row's first part: m and l, where the item's further
 // parts are, and how many there are (-1: none, and the output is written).
@@ -329,6 +333,7 @@ struct Shared {
     alignas(16) _Float16 scales[D / 16][4][16];  // [block][t / 4 % 4][t / 16 * 4 + t % 4]
     alignas(16) float k_scale[kTile];
     alignas(16) float v_scale[kTile];
+    float largest[16 * RT];  // of a row's weights, where the value scales are far apart
   };
   struct Merge {
     float o[WAVES][16][D + 4];
@@ -344,6 +349,9 @@ struct Shared {
 constexpr int groups_per_cu(int d, int rt) {
   return rt == 1 && d <= 128 ? (d == 64 ? 4 : 3) : 2;
 }
+
+// The same value in every lane, said so: descriptors and branches come from it.
+__device__ __forceinline__ int32_t same(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // Tiles [tile_lo, tile_hi) of an item; results to the output (more < 0: the
 // item is whole) or as a partial result (tile_lo 0: by row; else as further
@@ -369,8 +377,13 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) o[rt][dt] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
   }
-  // value scales up to `bound` times `norm` reach 2^15
-  float bound = 0.0f, norm = 1.0f;
+  // Value scales are held times 2^v_exp: up to `bound` they reach 2^14.  Once some lie far apart
+  // from others, or are not finite, `apart` is set, and every step takes care of each row.  (At
+  // every step without that flag it cost 1 to 3% of long contexts and 8% of many queries; so, 1%
+  // and 3%.)
+  float bound = 0.0f;
+  int v_exp = 0;
+  bool apart = false;
 
   // Pages: lane 4 k + j holds, for the 16 tokens j of step 16 n + k, the index of their first
   // cache row and of their first byte among the value scales of block 0.
@@ -568,25 +581,44 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
       const half2v a = e4m3_f16x2<0>(ve[j]), b = e4m3_f16x2<1>(ve[j]);
       *(half4v*)&tile.scales[e_lane / 4][e_lane % 4][j * 4] = (half4v){a[0], a[1], b[0], b[1]};
     }
-    const float vt_live = lane < left ? vt : 0.0f;
-    if (__any(vt_live > bound)) {
-      // a larger value scale than any before: a new power of two, with room for 8 times more
+    float vt_live = lane < left ? vt : 0.0f;
+    uint64_t broken = 0;  // tokens whose value scale is infinite or NaN
+    if (__any(!(vt_live <= bound) || (vt_live * kFar < bound && vt_live != 0.0f))) {
+      broken = __ballot(!(vt_live < INFINITY));
+      if (!(vt_live < INFINITY)) vt_live = 0.0f;
       const float top = max_of_groups(vt_live);
       float all = top;
 #pragma unroll
       for (int s = 8; s > 0; s /= 2) all = fmaxf(all, __shfl_xor(all, s));
-      const int ex = min(max(((int)(__float_as_uint(all) >> 23) & 255) - 126, -90) + 3, 120);
-      const float grown = __builtin_ldexpf(1.0f, ex);
-      const float shrink = bound == 0.0f ? 1.0f : bound / grown;
-      bound = grown;
-      norm = __builtin_ldexpf(1.0f, 15 - ex);
+      const bool before = apart;
+      int down = 0;
+      if (all > bound) {
+        // a larger value scale than any before: a new power of two, with room for 8 times more
+        const int ex = min(__builtin_amdgcn_frexp_expf(all) + 3, 127);
+        down = bound == 0.0f ? 0 : 14 - ex - v_exp;
+        if (!apart && bound == 0.0f) tile.largest[0] = __builtin_ldexpf(1.0f, ex);
+        bound = __builtin_ldexpf(1.0f, ex);
+        v_exp = 14 - ex;
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) o[rt][dt] *= shrink;
+          for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[rt][dt][i] = __builtin_ldexpf(o[rt][dt][i], down);
+      }
+      // Scales within 2^14 of the bound, or 2^20 of a later one, leave the weights of every row
+      // 2^23 of precision.  Any further apart, rows are kept apart as well (below).
+      apart = apart || broken != 0 || __any(vt_live * kFar < bound && vt_live != 0.0f) ||
+              tile.largest[0] * 0x1p6f < bound;
+      if (apart) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          tile.largest[rt * 16 + col] = __builtin_ldexpf(
+              before ? tile.largest[rt * 16 + col] : m[rt] == -INFINITY ? 0.0f : 0x1p14f, down);
+      }
     }
     tile.k_scale[lane] = __builtin_ldexpf(kt * factor_part, -lift);
-    tile.v_scale[lane] = vt_live * norm;
+    tile.v_scale[lane] = __builtin_ldexpf(vt_live, v_exp);
     if ((step + 1) % 16 == 0) load_pages(step + 1);
     locate(step + 1);
     load_values(step + 1);
@@ -642,13 +674,46 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
             __builtin_elementwise_maximum(top, s[rt][j][2]), s[rt][j][3]);
       }
       top = max_of_groups(top) * c_q[rt];
-      if (__any(!(top <= m[rt]))) {
+      if (__any(!(top <= m[rt])) || apart) {
         const float grown = __builtin_elementwise_maximum(m[rt], top);
         const float keep = m[rt] == -INFINITY ? 1.0f : factor(m[rt], grown);
         m[rt] = grown;
         l[rt] *= keep;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) o[rt][dt] *= keep;
+        if (apart) {
+          // The larger value scales may have no weight in this row, or not be seen by it: m is
+          // lowered until the row's largest weight is near 2^14, as far as l has room for that
+          // (2^100: sums of l over wavefronts and parts stay within FP32).  A row that sees an
+          // infinite or NaN scale becomes NaN.
+          const float from = m[rt] == -INFINITY ? 0.0f : m[rt];
+          float largest = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int token = 16 * j + 4 * grp + i;
+              const float e =
+                  __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][j][i], c_q[rt], -from));
+              largest = fmaxf(largest, e * tile.v_scale[token]);
+            }
+          const int seen = limit[rt] - t0;
+          const bool bad = seen > 0 && (broken << (64 - min(seen, 64))) != 0;
+          largest = fmaxf(max_of_groups(largest), tile.largest[rt * 16 + col] * keep);
+          int up = min(14 - __builtin_amdgcn_frexp_expf(largest),
+                       100 - __builtin_amdgcn_frexp_expf(max_of_groups(l[rt])));
+          // (past 2^22 a difference of 1 would be lost)
+          if (!(largest > 0.0f) || !(__builtin_fabsf(from) < 0x1p22f)) up = 0;
+          m[rt] -= up;
+          l[rt] = __builtin_ldexpf(l[rt], up);
+          tile.largest[rt * 16 + col] = __builtin_ldexpf(largest, up);
+          const float poison = bad ? __builtin_nanf("") : 0.0f;
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o[rt][dt][i] = __builtin_ldexpf(o[rt][dt][i], up) + poison;
+        }
       }
       const float base = m[rt] == -INFINITY ? 0.0f : m[rt];
 #pragma unroll
@@ -695,7 +760,6 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
   }
 
   // the wavefronts' results joined, 16 rows at a time; each thread takes pairs of one row
-  const float unscale = bound == 0.0f ? 0.0f : 1.0f / norm;
   const int tid = threadIdx.x, row_in = tid / (WAVES * 4), sub = tid % (WAVES * 4);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
@@ -704,7 +768,9 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
     const float sum = sum_of_groups(l[rt]);
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
-      *(float4v*)&sh.merge.o[wave][col][dt * 16 + grp * 4] = o[rt][dt] * unscale;
+      *(float4v*)&sh.merge.o[wave][col][dt * 16 + grp * 4] =
+          (float4v){__builtin_ldexpf(o[rt][dt][0], -v_exp), __builtin_ldexpf(o[rt][dt][1], -v_exp),
+                    __builtin_ldexpf(o[rt][dt][2], -v_exp), __builtin_ldexpf(o[rt][dt][3], -v_exp)};
     if (grp == 0) sh.merge.ml[wave][col] = make_float2(m[rt], sum);
     __syncthreads();
     const int r = rt * 16 + row_in;
@@ -762,9 +828,6 @@ __device__ __forceinline__ void own_item(const Params& p, int b, int rb, Item& j
   j.len = seen_by<RB>(p, j.own_len, rb);
   j.floor = max(0, j.own_len - p.q_tokens + 1 + (int)quotient(j.row0, p.per_head));
 }
-
-// The same value in every lane, said so: descriptors and branches come from it.
-__device__ __forceinline__ int32_t same(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 
 __device__ __forceinline__ void make_uniform(Item& j) {
   j.len = same(j.len);
