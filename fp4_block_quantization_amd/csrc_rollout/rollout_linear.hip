@@ -24,6 +24,8 @@
 // registers, one slab ahead of their use.  Small ones: the wavefronts of a
 // workgroup share 16 columns and divide k, so that even a few columns make
 // enough wavefronts without a second kernel to join them.
+#include <type_traits>
+
 #include "fp4q_device.h"
 #include "rollout_launch.h"
 
@@ -113,14 +115,17 @@ __global__ __launch_bounds__(64 * WAVES) void linear_dot(LinearArgs a, int64_t x
   load(0);
   for (int64_t c0 = 0; c0 < k; c0 += KC) {
     // The lane's four 16-byte pieces of a step lie at piece ^ (lane / 4 mod 4), so that 16
-    // lanes' reads, 64 bytes apart, meet all banks once; pieces past k repeat the last.
+    // lanes' reads, 64 bytes apart, meet all banks once; pieces past k are zeros.
     const int pieces = (int)min((int64_t)KC / 8, (k - c0) / 8), steps = (pieces + 255) / 256;
     if (c0 > 0) __syncthreads();
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       const uint16_t* x = (const uint16_t*)a.x + min((int64_t)r, a.rows - 1) * k + c0;
-      for (int i = threadIdx.x; i < steps * 256; i += 64 * WAVES)
-        *(u32x4v*)&xs[r][(i ^ (i / 16 % 4)) * 16] = *(const u32x4v*)(x + min(i, pieces - 1) * 8);
+      for (int i = threadIdx.x; i < steps * 256; i += 64 * WAVES) {
+        u32x4v v = *(const u32x4v*)(x + min(i, pieces - 1) * 8);
+        if (i >= pieces) v = (u32x4v){0, 0, 0, 0};
+        *(u32x4v*)&xs[r][(i ^ (i / 16 % 4)) * 16] = v;
+      }
     }
     __syncthreads();
     for (int s = 0; s < steps; ++s) {
@@ -248,12 +253,20 @@ __global__ __launch_bounds__(64 * WAVES) void linear_small(LinearArgs a) {
       s.w = (u32x4v){half[0], half[1], 0, 0};
       s.e = scales[step * 8];
     }
-    // pieces past k repeat the row's last one, times weights 0
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         s.x[r][q] = *(const u32x4v*)(x[r] + min(k0 + q * 8, k - 8));
+    if (step * 128 + 128 > k) {
+      // pieces past k are zeros: a weight of zero alone does not take an infinity away
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (k0 + q * 8 >= k) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) s.x[r][q] = (u32x4v){0, 0, 0, 0};
+        }
+    }
   };
   float4v acc[RT];
 #pragma unroll
@@ -416,8 +429,8 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
       for (int r = 0; r < RT; ++r) acc[t][r] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
 
     // a slab's activations: a copy fills 64 pieces; rows past the last are left as they are
-    // (their columns of the result are not stored), pieces past k repeat the last one (times
-    // weights 0)
+    // (their columns of the result are not stored), pieces past k repeat the last one and are
+    // not multiplied
     auto copy = [&](int slab) {
       const int64_t piece0 = (int64_t)slab * PIECES, last = k / 8 - 1;
 #pragma unroll
@@ -442,8 +455,8 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
         e_next[t].whole(scales[t] + (int64_t)slab * (KS / (MX ? 32 : 16)));
       }
     };
-    // the slab of w
-    auto multiply = [&](int slab, float (&f)[NT][STEPS][2]) {
+    // the slab of w; of k's last part, `left` elements
+    auto multiply = [&](int slab, float (&f)[NT][STEPS][2], auto last, int left) {
       const uint8_t* xb = xs[slab & 1] + at_piece;
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
@@ -454,6 +467,12 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
           for (int r = 0; r < RT; ++r)
             if (r == 0 || r * 16 < rows)
               xv[r] = *(const u32x4v*)(xb + r * 16 / PER_COPY * COPY + s * 64 + q * 16);
+          if constexpr (decltype(last)::value) {
+            // (a weight of zero alone does not take an infinity away)
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+              if (grp * (KS / 4) + s * 32 + q * 8 >= left) xv[r] = (u32x4v){0, 0, 0, 0};
+          }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             const bf16x8v wv = weights_of<MX>(w[t][s][q], f[t][s][MX ? 0 : q / 2]);
@@ -491,7 +510,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
       float f[NT][STEPS][2];
       begin(false, f);
       if (slab + 1 < slab_whole) load(slab + 1);
-      multiply(slab, f);
+      multiply(slab, f, std::false_type(), KS);
     }
     if (slab_whole < slab_hi) {
       const int left = (int)(k - (int64_t)slab_whole * KS);
@@ -515,7 +534,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
       }
       float f[NT][STEPS][2];
       begin(true, f);
-      multiply(slab_whole, f);
+      multiply(slab_whole, f, std::true_type(), left);
     }
 
     // lane (col, grp) holds columns n0 + 16 t + 4 grp + i of row m0 + 16 r + col
