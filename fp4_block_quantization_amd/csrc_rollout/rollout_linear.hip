@@ -161,10 +161,10 @@ __global__ __launch_bounds__(64 * WAVES) void linear_dot(LinearArgs a, int64_t x
           }
         }
         if constexpr (MX) {
-          const float f = __builtin_ldexpf(1.0f, (int)e_now[c] - 127);
+          // (a power of two of its own would leave FP32 at the highest byte)
 #pragma unroll
           for (int r = 0; r < ROWS; ++r)
-            sum[c][r] = __builtin_fmaf(part[0][r] + part[1][r], f, sum[c][r]);
+            sum[c][r] += __builtin_ldexpf(part[0][r] + part[1][r], (int)e_now[c] - 127);
         } else {
           const float f0 = e4m3_value<0>(e_now[c]), f1 = e4m3_value<1>(e_now[c]);
 #pragma unroll
@@ -195,6 +195,15 @@ __global__ __launch_bounds__(64 * WAVES) void linear_dot(LinearArgs a, int64_t x
 
 // ---- more rows ----------------------------------------------------------------
 
+// MXFP4 weights reach 6 * 2^128: the matrix forms take them times 2^-3, so that all are BF16
+// numbers, and scale the sums back.  The three lowest bytes leave the conversions' scale operand
+// then: slabs that have them are decoded by careful_weights, by which the small form decodes
+// all of them (testing for them took as long).
+constexpr uint32_t kMxDown = 3;
+constexpr float kMxUp = 8.0f;
+
+__device__ __forceinline__ float power_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
 // Eight weights of a word of codes as BF16, exact.  f: MXFP4's power of two,
 // or NVFP4's block scale.
 template <bool MX>
@@ -208,6 +217,23 @@ __device__ __forceinline__ bf16x8v weights_of(uint32_t word, float f) {
     const float2v c = e2m1x2_values<2>(word), d = e2m1x2_values<3>(word);
     const u32x4v w = {cvt_bf16x2(a[0] * f, a[1] * f), cvt_bf16x2(b[0] * f, b[1] * f),
                       cvt_bf16x2(c[0] * f, c[1] * f), cvt_bf16x2(d[0] * f, d[1] * f)};
+    return __builtin_bit_cast(bf16x8v, w);
+  }
+}
+
+// The same for any E8M0 byte, f = power_of(byte): times 2^-3.
+template <bool MX>
+__device__ __forceinline__ bf16x8v careful_weights(uint32_t word, float f) {
+  if constexpr (!MX) {
+    return weights_of<MX>(word, f);
+  } else {
+    const uint32_t byte = __float_as_uint(f) >> 23;
+    const float base = power_of(max(byte, kMxDown) - kMxDown);
+    const float rest = byte < kMxDown ? __builtin_ldexpf(1.0f, (int)byte - (int)kMxDown) : 1.0f;
+    const float2v a = e2m1x2_values_scaled<0>(word, base), b = e2m1x2_values_scaled<1>(word, base);
+    const float2v c = e2m1x2_values_scaled<2>(word, base), d = e2m1x2_values_scaled<3>(word, base);
+    const u32x4v w = {cvt_bf16x2(a[0] * rest, a[1] * rest), cvt_bf16x2(b[0] * rest, b[1] * rest),
+                      cvt_bf16x2(c[0] * rest, c[1] * rest), cvt_bf16x2(d[0] * rest, d[1] * rest)};
     return __builtin_bit_cast(bf16x8v, w);
   }
 }
@@ -276,11 +302,11 @@ __global__ __launch_bounds__(64 * WAVES) void linear_small(LinearArgs a) {
   for (int64_t step = wave; step < steps; step += WAVES) {
     const Step now = next;
     if (step + WAVES < steps) load(step + WAVES, next);
-    const float f0 = MX ? __uint_as_float(now.e << 23) : e4m3_value<0>(now.e);
+    const float f0 = MX ? power_of(now.e) : e4m3_value<0>(now.e);
     const float f1 = MX ? f0 : e4m3_value<1>(now.e);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const bf16x8v w = weights_of<MX>(now.w[q], q < 2 ? f0 : f1);
+      const bf16x8v w = careful_weights<MX>(now.w[q], q < 2 ? f0 : f1);
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[r] = product(w, now.x[r][q], acc[r]);
     }
@@ -297,7 +323,7 @@ __global__ __launch_bounds__(64 * WAVES) void linear_small(LinearArgs a) {
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) sum += sums[w][at / 16][at % 16];
-    put_out(a, m * a.n + to, MX ? sum : sum * a.row_scales[to]);
+    put_out(a, m * a.n + to, sum * (MX ? kMxUp : a.row_scales[to]));
   }
 }
 
@@ -328,13 +354,19 @@ struct ScaleLoad {
     for (int i = 0; i < BYTES; ++i)
       if (i < n) w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
   }
+  // MXFP4: whether a byte is below kMxDown, and all of them less kMxDown (if none is)
+  static constexpr uint32_t kDown = kMxDown * (BYTES == 2 ? 0x0101u : 0x01010101u);
+  __device__ __forceinline__ bool low() const {
+    return ((w[0] - kDown) & ~w[0] & (BYTES == 2 ? 0x8080u : 0x80808080u)) != 0;
+  }
+  __device__ __forceinline__ void lower() { w[0] -= kDown; }
   // The scale of the first (H = 0) and second 16 elements of step S; MXFP4's power of two, an
-  // FP32 pattern of which the conversions read the exponent field alone (so byte 0, 2^-127,
-  // works too), for both.
+  // FP32 pattern of which the conversions read the exponent field alone (so 0, 2^-127, works
+  // too), for both.
   template <int S, int H>
   __device__ __forceinline__ float value() const {
     if constexpr (MX)
-      return __uint_as_float((w[S / 4] >> (8 * (S % 4)) & 255u) << 23);
+      return power_of(w[S / 4] >> (8 * (S % 4)) & 255u);
     else
       return e4m3_value<(2 * S + H) % 4>(w[S / 2]);
   }
@@ -455,8 +487,10 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
         e_next[t].whole(scales[t] + (int64_t)slab * (KS / (MX ? 32 : 16)));
       }
     };
-    // the slab of w; of k's last part, `left` elements
-    auto multiply = [&](int slab, float (&f)[NT][STEPS][2], auto last, int left) {
+    // the slab of w, of which k has `left` elements; with care, these may be less than all of
+    // them, and scale bytes may be any
+    auto multiply = [&](int slab, float (&f)[NT][STEPS][2], auto care, int left) {
+      constexpr bool CARE = decltype(care)::value;
       const uint8_t* xb = xs[slab & 1] + at_piece;
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
@@ -467,7 +501,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
           for (int r = 0; r < RT; ++r)
             if (r == 0 || r * 16 < rows)
               xv[r] = *(const u32x4v*)(xb + r * 16 / PER_COPY * COPY + s * 64 + q * 16);
-          if constexpr (decltype(last)::value) {
+          if constexpr (CARE) {
             // (a weight of zero alone does not take an infinity away)
 #pragma unroll
             for (int r = 0; r < RT; ++r)
@@ -475,7 +509,9 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const bf16x8v wv = weights_of<MX>(w[t][s][q], f[t][s][MX ? 0 : q / 2]);
+            const float fv = f[t][s][MX ? 0 : q / 2];
+            const bf16x8v wv =
+                CARE ? careful_weights<MX>(w[t][s][q], fv) : weights_of<MX>(w[t][s][q], fv);
 #pragma unroll
             for (int r = 0; r < RT; ++r)
               if (r == 0 || r * 16 < rows) acc[t][r] = product(wv, xv[r], acc[t][r]);
@@ -483,8 +519,19 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
         }
       }
     };
-    auto begin = [&](bool turned, float (&f)[NT][STEPS][2]) {
+    // returns whether the slab needs care
+    auto begin = [&](bool turned, bool care, float (&f)[NT][STEPS][2]) {
       __builtin_amdgcn_s_waitcnt(0);  // this wavefront's copies and weights have landed
+      if constexpr (MX) {
+        bool low = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) low |= e_next[t].low();
+        care = care || __any(low);
+        if (!care) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) e_next[t].lower();
+        }
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -502,15 +549,19 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
         }
       }
       __syncthreads();  // the other wavefronts' copies too; the slab before is read
+      return care;
     };
 
     if (m0 != range.first) __syncthreads();  // the last rows' slabs are read
     if (slab_lo < slab_whole) load(slab_lo);
     for (int slab = slab_lo; slab < slab_whole; ++slab) {
       float f[NT][STEPS][2];
-      begin(false, f);
+      const bool care = begin(false, false, f);
       if (slab + 1 < slab_whole) load(slab + 1);
-      multiply(slab, f, std::false_type(), KS);
+      if (MX && care)
+        multiply(slab, f, std::true_type(), KS);
+      else
+        multiply(slab, f, std::false_type(), KS);
     }
     if (slab_whole < slab_hi) {
       const int left = (int)(k - (int64_t)slab_whole * KS);
@@ -533,7 +584,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
                        left / (MX ? 32 : 16) - grp * ScaleLoad<MX, KS>::BYTES);
       }
       float f[NT][STEPS][2];
-      begin(true, f);
+      begin(true, true, f);
       multiply(slab_whole, f, std::true_type(), left);
     }
 
@@ -559,7 +610,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 4 : 2) void linear_large(LinearArgs 
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (n + i < a.n) {
-            const float s = MX ? 1.0f : a.row_scales[matrix * a.n + n + i];
+            const float s = MX ? kMxUp : a.row_scales[matrix * a.n + n + i];
             put_out(a, m * a.n + n + i, acc[t][r][i] * s);
           }
       }
@@ -577,7 +628,7 @@ __global__ __launch_bounds__(256) void linear_join(LinearArgs a, int splits,
   float sum = 0.0f;
 #pragma unroll 4
   for (int s = 0; s < splits; ++s) sum += partial[s * all + at];
-  put_out(a, at, MX ? sum : sum * a.row_scales[at % a.n]);
+  put_out(a, at, sum * (MX ? kMxUp : a.row_scales[at % a.n]));
 }
 
 // ---- shape of a call ------------------------------------------------------------

@@ -62,7 +62,9 @@ FP4Q_API int64_t nvfp4_linear_workspace_bytes(int64_t rows, int64_t n, int64_t k
  * mxfp4_linear -- the same product for MXFP4 weights (the primary codes and
  * scales of mxfp4_resq_quantize): w = +-g(code) * 2^(byte - 127).
  *
- *   codes   uint8 [.., n, k/2], 16-byte aligned; scales uint8 [.., n, k/32] (E8M0).
+ *   codes   uint8 [.., n, k/2], 16-byte aligned; scales uint8 [.., n, k/32]
+ *           (E8M0): every byte is that power of two, 255 too, also where the
+ *           weight itself lies beyond FP32.
  *   k       a multiple of 32, up to 2^26.  Everything else: as for nvfp4_linear.
  */
 FP4Q_API fp4q_status mxfp4_linear(const void* x, int64_t rows, const uint8_t* codes,

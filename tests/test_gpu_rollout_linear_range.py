@@ -1,5 +1,5 @@
 """nvfp4_linear and mxfp4_linear at the ends of their inputs' range, in every
-form: an infinite activation in a row's last elements."""
+form: an infinite activation in a row's last elements, and every E8M0 byte."""
 import numpy as np
 import pytest
 import torch
@@ -67,3 +67,37 @@ def test_an_infinity_in_the_last_elements(mx, k, rows, grouped):
             assert np.array_equal(got[row], np.where(w[:, at] < 0, -np.inf, np.inf)), (at, row)
             keep = np.arange(rows) != row
             assert np.array_equal(got[keep], finite[keep])
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("k", [32, 96, 544, 4128])
+def test_every_scale_byte(k, rows, grouped):
+    # one byte a column: weights from 2^-128 (subnormal numbers of BF16) to 6 * 2^128, which
+    # neither BF16 nor FP32 holds; products with activations that bring them into FP32's range
+    codes = np.random.default_rng(k + rows).integers(0, 256, (256, k // 2)).astype(np.uint8)
+    scales = np.repeat(np.arange(256, dtype=np.uint8)[:, None], k // 32, 1)
+    w = ru.mx_values(codes, scales)
+    base = ru.bf16_values(workloads.random_rows(rows, rows, k))
+    for power, cols in ((100, slice(0, 100)), (0, slice(20, 230)), (-60, slice(90, 256))):
+        x = workloads.to_bf16_bits((base * 2.0 ** power).astype(np.float32))
+        got = run(True, x, (codes[cols], scales[cols]), grouped)
+        want, bound = product_bound(ru.bf16_values(x), w[cols])
+        ru.check(got, want, bound, "2^%d" % power)
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("rows", ROWS)
+def test_scale_bytes_of_a_column_far_apart(rows, grouped):
+    # neighbouring blocks from the lowest byte to the highest, met by activations to match
+    n, k = 48, 1056
+    rng = np.random.default_rng(rows)
+    codes = rng.integers(0, 256, (n, k // 2)).astype(np.uint8)
+    byte = rng.permutation(np.linspace(0, 255, k // 32).astype(np.int64))
+    scales = np.repeat(byte[None].astype(np.uint8), n, 0)
+    x = ru.bf16_values(workloads.random_rows(rows, rows, k))
+    x *= 2.0 ** np.repeat(np.clip(127 - byte, -110, 110), 32)[None]
+    x = workloads.to_bf16_bits(x.astype(np.float32))
+    got = run(True, x, (codes, scales), grouped)
+    want, bound = product_bound(ru.bf16_values(x), ru.mx_values(codes, scales))
+    ru.check(got, want, bound, "far apart")
