@@ -98,7 +98,10 @@ bool attention_shape_ok(int64_t page_size, int64_t kv_heads, int64_t head_dim, i
       max_prefix_pages > kMaxContext / page_size)
     return false;
   // query rows are numbered in 31 bits
-  return q_tokens == 0 || batch * q_heads <= kMaxSlots / q_tokens;
+  if (q_tokens > 0 && batch * q_heads > kMaxSlots / q_tokens) return false;
+  return batch == 0 || q_tokens == 0 ||
+         fp4q::kv_attention_fits(page_size, kv_heads, head_dim, batch, q_tokens, q_heads,
+                                 max_pages, max_prefix_pages, groups);
 }
 
 }  // namespace

@@ -96,6 +96,7 @@ struct Params {
   int32_t batch, q_tokens, q_heads, max_pages, max_prefix_pages, groups;
   int32_t blocks;  // row blocks of a sequence's own items
   int32_t parts;   // parts to cut all items into, about; 0: one workgroup per item
+  uint32_t first_block;  // number of the launch's first workgroup: a call may take several
   float scale;
 };
 
@@ -231,7 +232,7 @@ struct Spot {
   int share;
 };
 
-// The entry of part blockIdx.x: the tiles of all entries are summed, which
+// The entry of this workgroup's part: the tiles of all entries are summed, which
 // gives the parts' length, and then the entries' counts of parts are scanned.
 // All sums fit in 31 bits (the host's check).  Up to 64 entries, one a lane,
 // every wavefront does it by itself: this stands before anything else that a
@@ -239,7 +240,7 @@ struct Spot {
 template <int RB>
 __device__ __forceinline__ Spot find_part(const Params& p, int (&shared)[16]) {
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  const int entries = p.groups + p.batch, want = (int)blockIdx.x;
+  const int entries = p.groups + p.batch, want = (int)(p.first_block + blockIdx.x);
   Spot spot;
   int parts = 0, items = 0;
   auto count = [&](int n, int each_tiles) {
@@ -845,7 +846,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? groups_per_cu(D, RT)
                                          : D == 64  ? 4
                                                     : 2) void attention_items(Params p) {
   __shared__ Shared<D, RT, WAVES> sh;
-  const uint32_t block = blockIdx.x, pair = block / (uint32_t)p.kv_heads;
+  const uint32_t block = p.first_block + blockIdx.x, pair = block / (uint32_t)p.kv_heads;
   Item job;
   own_item<16 * RT>(p, (int)(pair / (uint32_t)p.blocks), (int)(pair % (uint32_t)p.blocks), job);
   job.kvh = (int)(block % (uint32_t)p.kv_heads);
@@ -862,7 +863,7 @@ __global__ __launch_bounds__(256, groups_per_cu(D, RT)) void attention_parts(Par
   const Spot spot = find_part<RB>(p, scratch);
   const int entry = same(spot.entry), share = same(spot.share);
   if (entry < 0) return;
-  int at = (int)blockIdx.x - same(spot.parts_before);  // the part's number in its entry
+  int at = (int)(p.first_block + blockIdx.x) - same(spot.parts_before);  // the part's number in its entry
   int further = same(spot.further_before);
   Item job;
   int tiles, item, n;
@@ -919,8 +920,9 @@ __global__ __launch_bounds__(256) void attention_join(Params p) {
   __shared__ float top_of[LANES], total_of[LANES];
   const int lane = threadIdx.x / COLS, d = threadIdx.x % COLS * 4;
   const int64_t per = ONE ? p.q_heads : (p.q_heads + LANES - 1) / LANES;
-  const int64_t bt = blockIdx.x / (uint32_t)per;
-  const int head = (int)(blockIdx.x - bt * per) * (ONE ? 1 : LANES) + (ONE ? 0 : lane);
+  const uint32_t block = p.first_block + blockIdx.x;
+  const int64_t bt = block / (uint32_t)per;
+  const int head = (int)(block - bt * per) * (ONE ? 1 : LANES) + (ONE ? 0 : lane);
   if (!ONE && (lane >= LANES || head >= p.q_heads)) return;
   const int64_t row = bt * p.q_heads + head;
   const First own = p.first[0][row];
@@ -1019,7 +1021,7 @@ struct Plan {
   int64_t blocks, items, rows;
   int64_t parts;   // 0: one workgroup per item
   int64_t groups;  // workgroups
-  bool fits;       // every count within 31 bits
+  bool fits;       // workgroups and tiles within 31 bits
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1064,45 +1066,69 @@ Plan plan_of(int64_t page_size, int64_t kv_heads, int64_t head_dim, int64_t batc
   p.groups = p.items + (p.parts ? p.parts + prefix_items : 0);
   const double tiles = (double)p.items * (double)ceil_div(tokens, kTile) +
                        (double)prefix_items * (double)ceil_div(max_prefix_pages * page_size, kTile);
-  // the dispatch packet counts work-items in 32 bits
-  p.fits = p.groups <= ((int64_t)1 << 31) / 512 && p.rows <= ((int64_t)1 << 31) / 256 &&
-           (p.parts == 0 || tiles < 2147483648.0);
+  p.fits = p.groups < ((int64_t)1 << 31) && (p.parts == 0 || tiles < 2147483648.0);
   return p;
 }
 
 int64_t first_parts(int64_t groups) { return groups ? 2 : 1; }
 
-template <int D, int RT>
-hipError_t join(const Params& p, const Plan& plan, hipStream_t stream) {
-  constexpr int64_t lanes = 256 / (D / 4);
-  // few rows: a workgroup for each, whose threads share its parts
-  if (plan.rows < 1024)
-    attention_join<D, RT, true><<<(uint32_t)plan.rows, 256, 0, stream>>>(p);
-  else
-    attention_join<D, RT, false><<<(uint32_t)(plan.rows / p.q_heads * ceil_div(p.q_heads, lanes)),
-                                   256, 0, stream>>>(p);
-  return hipGetLastError();
+// The dispatch packet counts work-items in 32 bits: larger calls go in several launches.
+constexpr int64_t kMaxItems = (int64_t)1 << 31;
+
+template <class F>
+hipError_t in_launches(Params& p, int64_t blocks, int threads, F launch_blocks) {
+  const int64_t step = kMaxItems / threads;
+  for (int64_t b0 = 0; b0 < blocks; b0 += step) {
+    p.first_block = (uint32_t)b0;
+    launch_blocks((uint32_t)(blocks - b0 < step ? blocks - b0 : step));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int D, int RT>
-hipError_t launch(const Params& p, const Plan& plan, hipStream_t stream) {
-  const uint32_t grid = (uint32_t)plan.groups;
+hipError_t join(Params& p, const Plan& plan, hipStream_t stream) {
+  constexpr int64_t lanes = 256 / (D / 4);
+  // few rows: a workgroup for each, whose threads share its parts
+  if (plan.rows < 1024)
+    return in_launches(p, plan.rows, 256, [&](uint32_t grid) {
+      attention_join<D, RT, true><<<grid, 256, 0, stream>>>(p);
+    });
+  return in_launches(p, plan.rows / p.q_heads * ceil_div(p.q_heads, lanes), 256,
+                     [&](uint32_t grid) {
+                       attention_join<D, RT, false><<<grid, 256, 0, stream>>>(p);
+                     });
+}
+
+template <int D, int RT>
+hipError_t launch(Params& p, const Plan& plan, hipStream_t stream) {
   if (plan.parts == 0) {
     if constexpr (RT == 1) {
-      if (plan.wide) {
-        attention_items<D, RT, 8><<<grid, 512, 0, stream>>>(p);
-        return hipGetLastError();
-      }
+      if (plan.wide)
+        return in_launches(p, plan.groups, 512, [&](uint32_t grid) {
+          attention_items<D, RT, 8><<<grid, 512, 0, stream>>>(p);
+        });
     }
-    attention_items<D, RT, 4><<<grid, 256, 0, stream>>>(p);
-    return hipGetLastError();
+    return in_launches(p, plan.groups, 256, [&](uint32_t grid) {
+      attention_items<D, RT, 4><<<grid, 256, 0, stream>>>(p);
+    });
   }
-  attention_parts<D, RT><<<grid, 256, 0, stream>>>(p);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = in_launches(p, plan.groups, 256, [&](uint32_t grid) {
+    attention_parts<D, RT><<<grid, 256, 0, stream>>>(p);
+  });
   return e != hipSuccess ? e : join<D, RT>(p, plan, stream);
 }
 
 }  // namespace
+
+bool kv_attention_fits(int64_t page_size, int64_t kv_heads, int64_t head_dim, int64_t batch,
+                       int64_t q_tokens, int64_t q_heads, int64_t max_pages,
+                       int64_t max_prefix_pages, int64_t groups) {
+  return plan_of(page_size, kv_heads, head_dim, batch, q_tokens, q_heads, max_pages,
+                 max_prefix_pages, groups)
+      .fits;
+}
 
 int64_t kv_attention_workspace_bytes(int64_t page_size, int64_t kv_heads, int64_t head_dim,
                                      int64_t batch, int64_t q_tokens, int64_t q_heads,
@@ -1119,7 +1145,6 @@ int64_t kv_attention_workspace_bytes(int64_t page_size, int64_t kv_heads, int64_
 hipError_t kv_attention_launch(const KvCache& c, const AttentionArgs& a, hipStream_t stream) {
   const Plan plan = plan_of(c.page_size, c.kv_heads, c.head_dim, a.batch, a.q_tokens, a.q_heads,
                             a.max_pages, a.max_prefix_pages, a.groups);
-  if (!plan.fits) return hipErrorInvalidValue;
   Params p;
   for (int i = 0; i < 2; ++i) {
     p.codes[i] = c.codes[i];

@@ -55,6 +55,11 @@ struct AttentionArgs {
   void* workspace;
 };
 
+// Whether a call's workgroups and the tiles that its tables have room for are counted in 31
+// bits, as the kernels count them.
+bool kv_attention_fits(int64_t page_size, int64_t kv_heads, int64_t head_dim, int64_t batch,
+                       int64_t q_tokens, int64_t q_heads, int64_t max_pages,
+                       int64_t max_prefix_pages, int64_t groups);
 int64_t kv_attention_workspace_bytes(int64_t page_size, int64_t kv_heads, int64_t head_dim,
                                      int64_t batch, int64_t q_tokens, int64_t q_heads,
                                      int64_t max_pages, int64_t max_prefix_pages, int64_t groups);

@@ -137,8 +137,13 @@ FP4Q_API fp4q_status nvfp4_kv_read(const uint8_t* k_codes, const uint8_t* k_scal
  *               at element (b * q_tokens + i) * q_stride; 16-byte aligned,
  *               q_stride a multiple of 8, at least q_heads * head_dim.
  *   q_heads     a positive multiple of kv_heads; head_dim 64, 128, 192 or 256.
- *   batch, q_tokens >= 0 (nothing is launched if either is 0).
+ *   batch, q_tokens >= 0 (nothing is launched if either is 0); batch and groups up to 65535,
+ *               batch * q_tokens * q_heads below 2^31.
  *   page_size   up to 2^27; max_pages and max_prefix_pages times page_size up to 2^30.
+ *               Where contexts are cut into parts (with groups, and for few sequences whose
+ *               tables have room for more than 2048 tokens) the room of all tables, in tiles of
+ *               64 tokens, times the blocks of 16 or 32 query rows and cache head that read it,
+ *               below 2^31.  Beyond these limits: FP4Q_ERROR_INVALID_SHAPE.
  *   page_table  int32 [batch, max_pages] on the device: page of the token
  *               o is page_table[b][o / page_size]; seq_lens int32 [batch],
  *               clamped to [0, max_pages * page_size].  Entries past a
