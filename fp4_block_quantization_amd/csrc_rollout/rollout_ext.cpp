@@ -40,10 +40,10 @@ struct Refused : std::runtime_error {
 
 [[noreturn]] void refuse(const std::string& what) { throw Refused(what); }
 
-std::string shape_of(const at::Tensor& t) {
-  std::string s = "(";
-  for (int64_t i = 0; i < t.dim(); ++i) s += (i ? ", " : "") + std::to_string(t.size(i));
-  return s + ")";
+std::string text_of(at::IntArrayRef sizes) {
+  std::string s = "[";
+  for (size_t i = 0; i < sizes.size(); ++i) s += (i ? ", " : "") + std::to_string(sizes[i]);
+  return s + "]";
 }
 
 const at::Tensor& tensor(PyObject* o, const char* name) {
@@ -71,6 +71,14 @@ const at::Tensor& sized(PyObject* o, const char* name, at::ScalarType type, int6
   if (t.numel() != numel)
     refuse(std::string(name) + " must hold " + std::to_string(numel) + " elements, got " +
            std::to_string(t.numel()));
+  return t;
+}
+
+const at::Tensor& shaped(PyObject* o, const char* name, at::ScalarType type,
+                         at::IntArrayRef sizes) {
+  const at::Tensor& t = dense(o, name, type);
+  if (t.sizes() != sizes)
+    refuse(std::string(name) + " must be " + text_of(sizes) + ", got " + text_of(t.sizes()));
   return t;
 }
 
@@ -141,24 +149,26 @@ PyObject* linear(PyObject* const* arg) {
   if (codes.dim() != (grouped ? 3 : 2))
     refuse("codes must be [n, k/2], or [groups, n, k/2] with offsets");
   const int64_t rows = x.size(0), k = x.size(1), n = codes.size(-2);
-  const int64_t groups = grouped ? codes.size(0) : 0, matrices = groups > 1 ? groups : 1;
+  const int64_t groups = grouped ? codes.size(0) : 0;
   if (codes.size(-1) * 2 != k)
     refuse("codes hold k = " + std::to_string(codes.size(-1) * 2) + ", x has " +
            std::to_string(k));
   const Device device(x);
   device.same(codes);
-  const at::Tensor& scales =
-      sized(arg[3], "scales", at::kByte, matrices * n * (k / (mx ? 32 : 16)));
+  // sizes of the scales, with and without the groups
+  const int64_t sizes[] = {groups, n, k / (mx ? 32 : 16)};
+  const int64_t* first = grouped ? sizes : sizes + 1;
+  const at::Tensor& scales = shaped(arg[3], "scales", at::kByte, {first, sizes + 3});
   device.same(scales);
   const float* row_scales = nullptr;
   if (!mx) {
-    const at::Tensor& t = sized(arg[4], "row_scales", at::kFloat, matrices * n);
+    const at::Tensor& t = shaped(arg[4], "row_scales", at::kFloat, {first, sizes + 2});
     device.same(t);
     row_scales = t.const_data_ptr<float>();
   }
   const int64_t* offsets = nullptr;
   if (grouped) {
-    const at::Tensor& t = sized(arg[5], "offsets", at::kLong, groups + 1);
+    const at::Tensor& t = shaped(arg[5], "offsets", at::kLong, {groups + 1});
     device.same(t);
     offsets = t.const_data_ptr<int64_t>();
   }
@@ -171,7 +181,7 @@ PyObject* linear(PyObject* const* arg) {
     if (t.scalar_type() != at::kFloat && t.scalar_type() != at::kBFloat16)
       refuse(std::string("out must be bfloat16 or float32, got ") + at::toString(t.scalar_type()));
     fp32 = t.scalar_type() == at::kFloat;
-    out = sized(arg[7], "out", t.scalar_type(), rows * n);
+    out = shaped(arg[7], "out", t.scalar_type(), {rows, n});
     device.same(out);
   }
   const Workspace ws(arg[8],
@@ -212,14 +222,16 @@ struct Cache {
       refuse("k_codes must be 4-D [pages, kv_heads, page_size, head_dim/2]");
     pages = first.size(0), heads = first.size(1), page = first.size(2), dim = 2 * first.size(3);
     device = first.device();
-    const int64_t rows = pages * heads * page;
     static const char* const names[] = {"k_codes", "k_scales", "k_token_scales",
                                         "v_codes", "v_scales", "v_token_scales"};
     const Device d(first);
     for (int i = 0; i < 2; ++i) {
-      const at::Tensor& c = sized(t[3 * i], names[3 * i], at::kByte, rows * (dim / 2));
-      const at::Tensor& s = sized(t[3 * i + 1], names[3 * i + 1], at::kByte, rows * (dim / 16));
-      const at::Tensor& f = sized(t[3 * i + 2], names[3 * i + 2], at::kFloat, rows);
+      const at::Tensor& c =
+          shaped(t[3 * i], names[3 * i], at::kByte, {pages, heads, page, dim / 2});
+      // (block scales of values: token innermost)
+      const at::Tensor& s = shaped(t[3 * i + 1], names[3 * i + 1], at::kByte,
+                                   {pages, heads, i ? dim / 16 : page, i ? page : dim / 16});
+      const at::Tensor& f = shaped(t[3 * i + 2], names[3 * i + 2], at::kFloat, {pages, heads, page});
       d.same(c);
       d.same(s);
       d.same(f);
@@ -235,7 +247,7 @@ struct Cache {
 int64_t token_stride(const at::Tensor& t, const char* name, int64_t heads, int64_t dim) {
   if (t.dim() < 3 || t.size(-2) != heads || t.size(-1) != dim)
     refuse(std::string(name) + " must be [..., " + std::to_string(heads) + ", " +
-           std::to_string(dim) + "], got " + shape_of(t));
+           std::to_string(dim) + "], got " + text_of(t.sizes()));
   if (t.is_contiguous()) return heads * dim;
   if ((dim > 1 && t.stride(-1) != 1) || (heads > 1 && t.stride(-2) != dim))
     refuse(std::string(name) + " must be dense over its last two dimensions");
@@ -289,8 +301,8 @@ PyObject* read(PyObject* const* arg) {
     v = device.empty({tokens, c.heads, c.dim}, at::kBFloat16);
   } else {
     if (!PyTuple_Check(arg[2]) || PyTuple_GET_SIZE(arg[2]) != 2) refuse("out must be (k, v)");
-    k = sized(PyTuple_GET_ITEM(arg[2], 0), "k", at::kBFloat16, tokens * c.heads * c.dim);
-    v = sized(PyTuple_GET_ITEM(arg[2], 1), "v", at::kBFloat16, tokens * c.heads * c.dim);
+    k = shaped(PyTuple_GET_ITEM(arg[2], 0), "k", at::kBFloat16, {tokens, c.heads, c.dim});
+    v = shaped(PyTuple_GET_ITEM(arg[2], 1), "v", at::kBFloat16, {tokens, c.heads, c.dim});
     device.same(k);
     device.same(v);
   }
@@ -320,7 +332,7 @@ PyObject* attention(PyObject* const* arg) {
   if (c.device != device.device) refuse("the cache must be on " + device.device.str());
   const at::Tensor& table = dense(arg[2], "page_table", at::kInt);
   if (table.dim() != 2 || table.size(0) != batch) refuse("page_table must be [batch, max_pages]");
-  const at::Tensor& lens = sized(arg[3], "seq_lens", at::kInt, batch);
+  const at::Tensor& lens = shaped(arg[3], "seq_lens", at::kInt, {batch});
   device.same(table);
   device.same(lens);
   double scale = 1.0 / std::sqrt((double)c.dim);
@@ -337,9 +349,9 @@ PyObject* attention(PyObject* const* arg) {
     if (t.dim() != 2 || t.size(0) == 0)
       refuse("prefix_table must be [groups, pages] with at least one group");
     groups = t.size(0), ppages = t.size(1);
-    const at::Tensor& l = sized(PyTuple_GET_ITEM(arg[5], 1), "prefix_lens", at::kInt, groups);
+    const at::Tensor& l = shaped(PyTuple_GET_ITEM(arg[5], 1), "prefix_lens", at::kInt, {groups});
     const at::Tensor& o =
-        sized(PyTuple_GET_ITEM(arg[5], 2), "group_offsets", at::kInt, groups + 1);
+        shaped(PyTuple_GET_ITEM(arg[5], 2), "group_offsets", at::kInt, {groups + 1});
     device.same(t);
     device.same(l);
     device.same(o);
@@ -351,7 +363,7 @@ PyObject* attention(PyObject* const* arg) {
   if (arg[7] == Py_None) {
     out = device.empty(q.sizes(), at::kBFloat16);
   } else {
-    out = sized(arg[7], "out", at::kBFloat16, q.numel());
+    out = shaped(arg[7], "out", at::kBFloat16, q.sizes());
     device.same(out);
   }
   at::Tensor lse;

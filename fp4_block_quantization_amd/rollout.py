@@ -106,10 +106,12 @@ def _fp32(out_dtype):
 def nvfp4_linear(x, codes, block_scales, row_scales, offsets=None, out_dtype=torch.bfloat16,
                  out=None, workspace=None):
     """x . DQ(W)^T of a BF16 [rows, k] tensor with NVFP4 weights as
-    nvfp4_quantize returns them for W [n, k].  With offsets (int64 GPU tensor
-    [experts + 1]) the weights are [experts, n, ..] and rows
-    [offsets[e], offsets[e+1]) go through expert e's; other rows of the
-    output are not written.  out: optional bfloat16 or float32 [rows, n]."""
+    nvfp4_quantize returns them for W [n, k]: codes [n, k/2], block_scales
+    [n, k/16], row_scales [n].  With offsets (int64 GPU tensor [experts + 1])
+    each is [experts, n, ..] and rows [offsets[e], offsets[e+1]) go through
+    expert e's; other rows of the output are not written.  out: optional
+    bfloat16 or float32 [rows, n].  Tensors of another shape are refused, also
+    where they hold as many elements."""
     return (_ext or _native()).linear(False, x, codes, block_scales, row_scales, offsets,
                                       _fp32(out_dtype), out, workspace)
 
@@ -125,7 +127,8 @@ def mxfp4_linear(x, codes, scales, offsets=None, out_dtype=torch.bfloat16, out=N
 NvFp4KvCache = namedtuple("NvFp4KvCache", "k_codes k_scales k_token_scales "
                                           "v_codes v_scales v_token_scales")
 NvFp4KvCache.__doc__ = """A paged NVFP4 key/value cache: k_codes, v_codes u8
-[pages, kv_heads, page_size, d/2]; k_scales u8 [pages, kv_heads, page_size,
+[pages, kv_heads, page_size, d/2] (d a multiple of 16; attention takes 64,
+128, 192 and 256); k_scales u8 [pages, kv_heads, page_size,
 d/16]; v_scales u8 [pages, kv_heads, d/16, page_size]; k_token_scales,
 v_token_scales f32 [pages, kv_heads, page_size].  Token slot p * page_size + o
 is place o of page p."""
