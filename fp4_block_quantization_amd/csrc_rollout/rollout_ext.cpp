@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -82,6 +83,13 @@ const at::Tensor& shaped(PyObject* o, const char* name, at::ScalarType type,
   return t;
 }
 
+// There is no backward pass: a result without history is no answer to an input that asks for one.
+void no_gradient(const at::Tensor& t, const char* name) {
+  if (t.requires_grad() && at::GradMode::is_enabled())
+    refuse(std::string(name) + " requires a gradient, which this call does not have: detach it, "
+                               "or call under torch.no_grad()");
+}
+
 // The device that every tensor of a call is on.
 struct Device {
   c10::Device device;
@@ -144,6 +152,7 @@ PyObject* linear(PyObject* const* arg) {
   const bool mx = truth(arg[0]);
   const at::Tensor& x = dense(arg[1], "x", at::kBFloat16);
   const at::Tensor& codes = dense(arg[2], "codes", at::kByte);
+  no_gradient(x, "x");
   if (x.dim() != 2) refuse("x must be 2-D [rows, k]");
   const bool grouped = arg[5] != Py_None;
   if (codes.dim() != (grouped ? 3 : 2))
@@ -164,6 +173,7 @@ PyObject* linear(PyObject* const* arg) {
   if (!mx) {
     const at::Tensor& t = shaped(arg[4], "row_scales", at::kFloat, {first, sizes + 2});
     device.same(t);
+    no_gradient(t, "row_scales");
     row_scales = t.const_data_ptr<float>();
   }
   const int64_t* offsets = nullptr;
@@ -235,6 +245,7 @@ struct Cache {
       d.same(c);
       d.same(s);
       d.same(f);
+      no_gradient(f, names[3 * i + 2]);
       codes[i] = c.data_ptr<uint8_t>();
       scales[i] = s.data_ptr<uint8_t>();
       token_scales[i] = f.data_ptr<float>();
@@ -269,6 +280,8 @@ PyObject* append(PyObject* const* arg) {
   const Cache c(arg[0]);
   const at::Tensor& k = typed(arg[1], "k", at::kBFloat16);
   const at::Tensor& v = typed(arg[2], "v", at::kBFloat16);
+  no_gradient(k, "k");
+  no_gradient(v, "v");
   const int64_t ks = token_stride(k, "k", c.heads, c.dim);
   const int64_t vs = token_stride(v, "v", c.heads, c.dim);
   if (k.numel() != v.numel()) refuse("k and v must hold the same tokens");
@@ -323,6 +336,7 @@ PyObject* read(PyObject* const* arg) {
 //   -> out, or (out, lse)
 PyObject* attention(PyObject* const* arg) {
   const at::Tensor& q = typed(arg[0], "q", at::kBFloat16);
+  no_gradient(q, "q");
   const Cache c(arg[1]);
   if (q.dim() != 3 && q.dim() != 4)
     refuse("q must be [batch, tokens, heads, head_dim] or [batch, heads, head_dim]");

@@ -5,7 +5,8 @@ Argument marshalling only, in the manner of the package's other calls: GPU
 tensors in, outputs allocated on the inputs' device or passed in, launches
 on torch's current stream, no CPU fallback.  The checks are in a native
 module (csrc_rollout/rollout_ext.cpp): in Python they took longer than the
-smaller kernels run.
+smaller kernels run.  There is no backward pass: in grad mode an input that
+requires a gradient is refused.
 
   nvfp4_linear(x, codes, block_scales, row_scales, offsets=None) -> [R, N]
   mxfp4_linear(x, codes, scales, offsets=None) -> [R, N]

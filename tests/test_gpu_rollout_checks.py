@@ -1,5 +1,6 @@
 """The rollout binding's checks: tensors that hold the right number of
-elements in another shape are refused, not misread."""
+elements in another shape are refused, not misread, and so are inputs that
+ask for a gradient."""
 import pytest
 import torch
 
@@ -97,3 +98,29 @@ def test_attention_shapes():
                dict(prefix=(prefix[0], prefix[1], prefix[2].view(2, 2)))):
         with pytest.raises(fq.Fp4qError):
             fq.nvfp4_kv_attention(**{**dict(q=q, cache=cache, page_table=table, seq_lens=lens), **kw})
+
+
+def test_gradients_are_refused():
+    cache = fq.nvfp4_kv_cache(4, 32, 2, 64)
+    slots, table, lens = ints(torch.int64, 3), ints(torch.int32, 3, 2), ints(torch.int32, 3)
+    w = (u8(8, 32), u8(8, 4), f32(8))
+    mxw = (u8(8, 32), u8(8, 2))
+    asks = lambda t: t.clone().requires_grad_()
+    x, row, q = bf16(6, 64), bf16(3, 2, 64), bf16(3, 4, 64)
+    learnt = cache._replace(k_token_scales=asks(cache.k_token_scales))
+    calls = [lambda: fq.nvfp4_linear(asks(x), *w), lambda: fq.mxfp4_linear(asks(x), *mxw),
+             lambda: fq.nvfp4_linear(x, w[0], w[1], asks(w[2])),
+             lambda: fq.nvfp4_linear(asks(x) * 2, *w),  # not a leaf
+             lambda: fq.nvfp4_kv_append(cache, asks(row), row, slots),
+             lambda: fq.nvfp4_kv_append(cache, row, asks(row), slots),
+             lambda: fq.nvfp4_kv_attention(asks(q), cache, table, lens),
+             lambda: fq.nvfp4_kv_attention(q, learnt, table, lens),
+             lambda: fq.nvfp4_kv_read(learnt, slots)]
+    for call in calls:
+        with pytest.raises(fq.Fp4qError, match="gradient"):
+            call()
+        with torch.no_grad():
+            call()
+        with torch.inference_mode():
+            call()
+    assert not fq.nvfp4_linear(asks(x).detach(), *w).requires_grad
