@@ -96,33 +96,37 @@ def bind(ext, L):
              *[ctypes.cast(c, ctypes.c_void_p).value for c in calls])
 
 
-def _fp32(out_dtype):
-    if out_dtype is torch.bfloat16:
+def _fp32(out_dtype, out):
+    if out is not None:
+        if out_dtype is not None and out_dtype is not getattr(out, "dtype", None):
+            raise Fp4qError("out is not of out_dtype %s" % (out_dtype,))
+        return False  # out's own type decides
+    if out_dtype is None or out_dtype is torch.bfloat16:
         return False
     if out_dtype is torch.float32:
         return True
     raise Fp4qError("out_dtype must be torch.bfloat16 or torch.float32, got %s" % (out_dtype,))
 
 
-def nvfp4_linear(x, codes, block_scales, row_scales, offsets=None, out_dtype=torch.bfloat16,
-                 out=None, workspace=None):
+def nvfp4_linear(x, codes, block_scales, row_scales, offsets=None, out_dtype=None, out=None,
+                 workspace=None):
     """x . DQ(W)^T of a BF16 [rows, k] tensor with NVFP4 weights as
     nvfp4_quantize returns them for W [n, k]: codes [n, k/2], block_scales
     [n, k/16], row_scales [n].  With offsets (int64 GPU tensor [experts + 1])
     each is [experts, n, ..] and rows [offsets[e], offsets[e+1]) go through
-    expert e's; other rows of the output are not written.  out: optional
-    bfloat16 or float32 [rows, n].  Tensors of another shape are refused, also
+    expert e's; other rows of the output are not written.  out_dtype:
+    bfloat16 (default) or float32; out: optional [rows, n] of either, whose
+    type decides.  Tensors of another shape are refused, also
     where they hold as many elements."""
     return (_ext or _native()).linear(False, x, codes, block_scales, row_scales, offsets,
-                                      _fp32(out_dtype), out, workspace)
+                                      _fp32(out_dtype, out), out, workspace)
 
 
-def mxfp4_linear(x, codes, scales, offsets=None, out_dtype=torch.bfloat16, out=None,
-                 workspace=None):
+def mxfp4_linear(x, codes, scales, offsets=None, out_dtype=None, out=None, workspace=None):
     """x . DQ(W)^T with MXFP4 weights (the primary codes and scales of
     mxfp4_resq_quantize); otherwise as nvfp4_linear."""
-    return (_ext or _native()).linear(True, x, codes, scales, None, offsets, _fp32(out_dtype),
-                                      out, workspace)
+    return (_ext or _native()).linear(True, x, codes, scales, None, offsets,
+                                      _fp32(out_dtype, out), out, workspace)
 
 
 NvFp4KvCache = namedtuple("NvFp4KvCache", "k_codes k_scales k_token_scales "

@@ -124,3 +124,24 @@ def test_gradients_are_refused():
         with torch.inference_mode():
             call()
     assert not fq.nvfp4_linear(asks(x).detach(), *w).requires_grad
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_out_and_out_dtype(mx):
+    x, w = bf16(6, 64), (u8(8, 32), u8(8, 2)) if mx else (u8(8, 32), u8(8, 4), f32(8))
+    call = fq.mxfp4_linear if mx else fq.nvfp4_linear
+    assert call(x, *w).dtype is torch.bfloat16
+    for dtype in (torch.bfloat16, torch.float32):
+        out = torch.empty((6, 8), dtype=dtype, device="cuda")
+        assert call(x, *w, out_dtype=dtype).dtype is dtype
+        assert call(x, *w, out=out).data_ptr() == out.data_ptr()
+        assert call(x, *w, out_dtype=dtype, out=out).dtype is dtype
+        other = torch.float32 if dtype is torch.bfloat16 else torch.bfloat16
+        for wrong in (other, torch.float16):
+            with pytest.raises(fq.Fp4qError):
+                call(x, *w, out_dtype=wrong, out=out)
+    with pytest.raises(fq.Fp4qError):
+        call(x, *w, out_dtype=torch.float16)
+    for kw in (dict(), dict(out_dtype=torch.float32)):
+        with pytest.raises(fq.Fp4qError):
+            call(x, *w, out=[1.0], **kw)
