@@ -212,18 +212,22 @@ PyObject* linear(PyObject* const* arg) {
   return THPVariable_Wrap(std::move(out));
 }
 
+// Holds its six tensors for the length of the call: a sequence may make them as it is read, and
+// what the call allocates must not take their memory.
 struct Cache {
+  struct Held {
+    PyObject* p;
+    ~Held() { Py_XDECREF(p); }
+  } held;
   uint8_t *codes[2], *scales[2];
   float* token_scales[2];
   int64_t pages, heads, page, dim;
   c10::Device device{c10::kCPU};
-  explicit Cache(PyObject* o) {
-    PyObject* seq = PySequence_Fast(o, "cache must be an NvFp4KvCache, or its six tensors");
+  Cache(const Cache&) = delete;
+  explicit Cache(PyObject* o)
+      : held{PySequence_Fast(o, "cache must be an NvFp4KvCache, or its six tensors")} {
+    PyObject* seq = held.p;
     if (!seq) throw Raised();
-    struct Release {
-      PyObject* p;
-      ~Release() { Py_DECREF(p); }
-    } release{seq};
     if (PySequence_Fast_GET_SIZE(seq) != 6)
       refuse("cache must be an NvFp4KvCache, or its six tensors in order");
     PyObject** t = PySequence_Fast_ITEMS(seq);

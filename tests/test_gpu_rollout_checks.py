@@ -145,3 +145,20 @@ def test_out_and_out_dtype(mx):
     for kw in (dict(), dict(out_dtype=torch.float32)):
         with pytest.raises(fq.Fp4qError):
             call(x, *w, out=[1.0], **kw)
+
+
+def test_a_cache_made_as_it_is_read():
+    # its tensors live as long as the call: the outputs must not take their memory
+    cache = fq.nvfp4_kv_cache(8, 32, 2, 64)
+    rows = [torch.randn((256, 2, 64), device="cuda").bfloat16() for _ in range(2)]
+    slots = torch.arange(256, device="cuda")
+    fq.nvfp4_kv_append(cache, *rows, slots)
+    want = fq.nvfp4_kv_read(cache, slots)
+    table = torch.arange(8, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([250], dtype=torch.int32, device="cuda")
+    q = torch.randn((1, 4, 64), device="cuda").bfloat16()
+    attended = fq.nvfp4_kv_attention(q, cache, table, lens)
+    for _ in range(5):
+        for a, b in zip(fq.nvfp4_kv_read((t.clone() for t in cache), slots), want):
+            assert torch.equal(a, b)
+        assert torch.equal(fq.nvfp4_kv_attention(q, (t.clone() for t in cache), table, lens), attended)
