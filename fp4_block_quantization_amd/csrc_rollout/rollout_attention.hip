@@ -380,8 +380,8 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
   }
   // Value scales are held times 2^v_exp: up to `bound` they reach 2^14.  Once some lie far apart
   // from others, or are not finite, `apart` is set, and every step takes care of each row.  (At
-  // every step without that flag it cost 1 to 3% of long contexts and 8% of many queries; so, 1%
-  // and 3%.)
+  // every step without that flag it cost 1 to 3% of long contexts and 8% of many queries; so, up to
+  // 1% and 2%.)
   float bound = 0.0f;
   int v_exp = 0;
   bool apart = false;
@@ -596,21 +596,25 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
       if (all > bound) {
         // a larger value scale than any before: a new power of two, with room for 8 times more
         const int ex = min(__builtin_amdgcn_frexp_expf(all) + 3, 127);
-        down = bound == 0.0f ? 0 : 14 - ex - v_exp;
-        if (!apart && bound == 0.0f) tile.largest[0] = __builtin_ldexpf(1.0f, ex);
-        bound = __builtin_ldexpf(1.0f, ex);
+        const float grown = __builtin_ldexpf(1.0f, ex);
+        if (__any(bound == 0.0f)) {  // the first
+          if (!apart) tile.largest[0] = grown;
+        } else {
+          down = 14 - ex - v_exp;
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[rt][dt][i] = __builtin_ldexpf(o[rt][dt][i], down);
+          apart = apart || __any(tile.largest[0] * 0x1p6f < grown);
+        }
+        bound = grown;
         v_exp = 14 - ex;
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[rt][dt][i] = __builtin_ldexpf(o[rt][dt][i], down);
       }
       // Scales within 2^14 of the bound, or 2^20 of a later one, leave the weights of every row
       // 2^23 of precision.  Any further apart, rows are kept apart as well (below).
-      apart = apart || broken != 0 || __any(vt_live * kFar < bound && vt_live != 0.0f) ||
-              tile.largest[0] * 0x1p6f < bound;
+      apart = apart || broken != 0 || __any(vt_live * kFar < bound && vt_live != 0.0f);
       if (apart) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
