@@ -6,7 +6,7 @@
 // the products g e are FP16 numbers (at most 6 significant bits, 2^-10 to
 // 2688), so the matrix units take them as they are:
 //   S[t][q] = sum_d (g e)[t][d] q[d]       q scaled by a power of two into
-//                                          FP16's range, exactly
+//                                          FP16's range
 //   x = (S (s_t f)) c_q                    scale log2(e) = f 2^n; c_q: 2^n, q's power of two
 //   p = 2^(x - m), l += p, m the running maximum of x
 //   O[d][q] += sum_t (g' e')[t][d] w,  w = FP16(p s'_t / b)
@@ -30,7 +30,7 @@
 // Work.  One wavefront takes a tile of 64 tokens at a time and up to
 // 16 * RT query rows of one cache head (a sequence's queries and the heads
 // that share the cache head; for a prefix, those of all sequences of the
-// group, so that the prefix is read once per 16 * RT of them).  The WAVES
+// group, so that the prefix is read and decoded once per 16 * RT of them).  The WAVES
 // wavefronts of a workgroup take an item's tiles in turn and merge their
 // (m, l, O) through LDS.  Short contexts take one workgroup per item.  Longer
 // ones are cut into parts of about equal length, one for each workgroup: the
@@ -39,13 +39,14 @@
 // joins the parts of an item in a fixed order.
 //
 // What bounds it.  Long contexts: the cache's bytes.  64 sequences of 64
-// heads over 8 of 128, 2048 to 8192 tokens each (400 MB), take 95 us, 4.2
-// TB/s; the longer the contexts the nearer to 88% of a copy's rate, as some
-// 18 us are the launch, the first loads (table, then tokens), the last parts
-// and the join.  Prompts shared by 16 sequences: decoding, repeated for each
-// 16 rows (48 us; one read of the bytes would take 12).  Small batches: 4 us
-// without any token, and 3 for each of a wavefront's steps, whose chain of
-// scores, softmax and values few wavefronts do not cover (777 tokens 10.5).
+// heads over 8 of 128 take 90 us with 5120 tokens each and 164 with 10240: 84%
+// of a copy's rate, and 16 us for the launch, the first loads (length, table and
+// queries, tokens, each behind the one before), the last parts and the join.
+// 2048 to 8192 tokens (400 MB as well) take 97 us, as unequal contexts' parts are
+// unequal too.  Prompts shared by 16 sequences: decoding, repeated for each 16
+// rows (49 us; one read of the bytes would take 12).  Small batches: some 7 us for
+// a context of one tile, and 3 for each further step of a wavefront, whose chain
+// of scores, softmax and values few wavefronts do not cover (777 tokens 10.7).
 #include "fp4q_device.h"
 #include "rollout_divisor.h"
 #include "rollout_launch.h"
@@ -485,8 +486,9 @@ __device__ __forceinline__ void attend(const Params& p, const Item& job, int til
     return __builtin_amdgcn_ds_read_tr4_b64_v2i32(
         (__attribute__((address_space(3))) int2v*)(tile.codes + turned * kVRow + dt * 8));
   };
-  // The page table, the queries and the first tile are asked for before anything is done
-  // with them.  Queries: lane (col, grp) holds row col's elements [grp D/4, (grp + 1) D/4).
+  // The page table, then the queries, then the first tile are asked for (each waits for the one
+  // before: the table entry is made into addresses at once, and a row that does not exist is a
+  // branch).  Queries: lane (col, grp) holds row col's elements [grp D/4, (grp + 1) D/4).
   u32x4v raw[RT][NK];
   int limit[RT];
   if (job.pages > 0) load_pages(0);
@@ -952,7 +954,7 @@ __global__ __launch_bounds__(256) void attention_join(Params p) {
     const int more =
         (uint32_t)first.next < (uint32_t)p.parts ? min(first.more, p.parts - first.next) : 0;
     // some parts at a time, so that their loads are in flight together (one context of 32k
-    // tokens 21.1 -> 19.7 us)
+    // tokens 19.7 us, one part at a time 21.1)
     constexpr int STEP = ONE ? LANES : 1, MANY = 4;
     for (int i = ONE ? lane : 0; i < more; i += STEP * MANY) {
       float2 ml[MANY];
@@ -1039,9 +1041,9 @@ Plan plan_of(int64_t page_size, int64_t kv_heads, int64_t head_dim, int64_t batc
   // One row tile a workgroup, or two that share what they decode.  Two from heads of 192 on would
   // take 416 registers and more: one workgroup per CU (16 sequences a prompt of 8192, heads of
   // 256: 80 us with one, 116 with two).  Groups: one up to 256 rows each (4 x 64 rows x 8192 tokens
-  // 49 us with one, 51 with two; 4 x 512 rows x 16384 301 and 266).  Without groups: two where
+  // 49 us with one, 52 with two; 4 x 512 rows x 16384 318 and 276).  Without groups: two where
   // a tile would not hold a sequence's and twos are enough for all CUs (64 sequences x 64 rows x
-  // 2000 tokens 64 us with two, 80 with one; 4 such sequences 25 and 17)
+  // 512-2000 tokens 66 us with two, 75 with one; 4 such sequences 27 and 17)
   const bool two = groups ? rows_each > 256
                           : per_seq > 16 && batch * ceil_div(per_seq, 32) * kv_heads >= 256;
   p.rt = head_dim <= 128 && two ? 2 : 1;
@@ -1051,17 +1053,17 @@ Plan plan_of(int64_t page_size, int64_t kv_heads, int64_t head_dim, int64_t batc
   const int64_t held = 256 * groups_per_cu((int)head_dim, p.rt);
   const int64_t tokens = max_pages * page_size;
   // One row tile: eight wavefronts a workgroup where the chip holds all of them at once (128
-  // items of heads of 128, up to 700 tokens: 9.3 us with eight, 10.9 with four), else four
-  // (512 items of 512 tokens 19.8 and 13.8, 2048 of 30-500 58 and 32)
+  // items of heads of 128, 100-700 tokens: 9.7 us with eight, 11.1 with four), else four
+  // (512 items of 512 tokens 19.8 and 14.2, 2048 of 30-500 60 and 34)
   p.wide = p.rt == 1 && p.items <= (head_dim == 64 ? 512 : 256);
-  // One workgroup per item where the contexts are short (a join costs about 5 us: 777 tokens
-  // 10.4 us so, 14.3 cut), also longer ones where items keep all CUs busy (512 of 2000-4000
-  // tokens 54 and 64, 256 of 1000-4000 29 and 37, 64 of 2000-4000 26 and 19; but one of 3900
-  // among 300s 34 and 21), or the items so many that their
-  // unequal lengths even out.  Else as many parts as the chip holds workgroups; twice as many
-  // where one tile holds a sequence's rows (64 x 2048-8192 tokens: 98 us, 102 with one); two a CU
-  // with groups, whose rows are many to join (4 x 256 rows x 8192 tokens 61 us, 72 with one a CU,
-  // 61 with three; 4 x 64 rows 49, 46 and 49; the same with heads of 64 33, 36 and 36)
+  // One workgroup per item where the contexts are short (777 tokens 10.8 us so, 13.4 cut), also
+  // longer ones where items keep all CUs busy (512 of 2000-4000 tokens 56 and 65, 256 of 1000-4000
+  // 30 and 37; but 64 of 2000-4000 27 and 19, and 8 of such a length among 56 of 300 tokens 23 and
+  // 14), or the items so many that their unequal lengths even out.  Else as many parts as the chip
+  // holds workgroups; twice as many where one tile holds a sequence's rows (64 x 2048-8192 tokens:
+  // 97 us, 101 with one); two a CU with groups, whose rows are many to join (4 x 256 rows x 8192
+  // tokens 63 us, 73 with one a CU, 64 with three; 4 x 64 rows 50, 46 and 50; the same with heads
+  // of 64 34, 37 and 37)
   p.parts = groups ? 512
             : tokens <= (p.items >= 256 ? 4096 : 2048) || p.items >= 8 * held ? 0
             : per_seq <= 16 ? 2 * held : held;

@@ -3,8 +3,8 @@
 //
 // All forms read every weight byte once per 16 * RT (or ROWS) rows of x
 // and are bound by that read: 0.5625 bytes a weight (NVFP4), 0.53 (MXFP4).
-// 65536 x 7168 (264 MB): one row 50 us (5.3 TB/s), 16 rows 63, 64 rows 95
-// (0.63 PFLOP/s).
+// 65536 x 7168 (264 MB): one row 52 us (5.1 TB/s), 16 rows 65 (66 to 71 on other
+// boxes), 64 rows 100 (0.6 PFLOP/s).
 //
 // One or two rows (dot form).  A wavefront takes NC output columns; a lane
 // takes 32 consecutive weights of a column at a time (16 bytes of codes, so a
@@ -14,9 +14,9 @@
 //
 // More rows (matrix form).  Weights are the rows of a 16x16x32 matrix
 // instruction, activations its columns.  A weight enters as an exact BF16
-// number: g e of NVFP4 has at most 6 significant bits, g 2^E of MXFP4 at
-// most 2 (the conversion's own scale operand gives it), and the activations
-// enter as they are.  Widening to FP16 instead takes half the vector
+// number: g e of NVFP4 has at most 6 significant bits, g 2^E of MXFP4 (times
+// 2^-3) at most 2 (the conversion's own scale operand gives it), and the
+// activations enter as they are.  Widening to FP16 instead takes half the vector
 // instructions an NVFP4 weight (packed products), but then the activations
 // have to be brought into FP16's range by a kernel before, which costs more
 // than it gives.  Large matrices: slabs of the activations are copied to
@@ -373,8 +373,7 @@ struct ScaleLoad {
 };
 
 // The matrix instruction wants a column a lane, but loaded so every lane's 16 bytes are an
-// access of their own, 64 a load, and the vector memory pipe was busy for most of the time.  So N
-// neighbouring lanes read N * 16 consecutive bytes of one column, for N columns in turn, and this
+// access of their own, 64 a load.  So N neighbouring lanes read N * 16 consecutive bytes of one column, for N columns in turn, and this
 // is the transposition: w[r] of lane b of N becomes what lane r had in w[b].  (32 experts x 8 rows
 // 67 -> 61 us, 65536 x 7168 by 16 rows 71 -> 63; exchanged through LDS 63 and 64; two slabs of
 // weights ahead instead of one 62 and 65.)
@@ -651,7 +650,7 @@ Plan plan_of(int64_t rows, int64_t n, int64_t k, int64_t groups) {
     p.form = Form::kDot;
     p.rows = (int)rows;
     // one column a wavefront fills the chip best (2048 x 7168: 5.2, 5.8 with two); where
-    // columns abound, two share the activations' reads (65536 x 7168: 50, 56 with one)
+    // columns abound, two share the activations' reads (65536 x 7168: 52, 56 with one)
     p.nt = rows == 2 || n >= 16384 ? 2 : 1;
     return p;
   }
@@ -666,16 +665,16 @@ Plan plan_of(int64_t rows, int64_t n, int64_t k, int64_t groups) {
     return p;
   }
   // Each wavefront of the small form goes through k / 1024 steps a row tile on its own, and
-  // reads all activations: 8 rows, 4096 x 4096 6.6 (large form 9.0), 2048 x 2048 4.4 (7.9),
-  // but 1024 x 7168 9.2 (8.7), 16384 x 2048 11.4 (11.3); 24 rows, 2048 x 2048 6.3 (7.3), but
-  // 7168 x 2048 10.5 (9.6)
+  // reads all activations: 8 rows, 4096 x 4096 6.7 (large form 8.8), 2048 x 2048 4.4 (7.9),
+  // but 1024 x 7168 9.1 (8.5), 16384 x 2048 11.2 (11.4); 24 rows, 2048 x 2048 6.2 (7.0), but
+  // 7168 x 2048 10.4 (9.3)
   const int64_t row_tiles = ceil_div(rows, 16);
   if (k * row_tiles <= 4096 && n * k * row_tiles <= ((int64_t)1 << 24)) {
     p.form = Form::kSmall;
     return p;
   }
   // above 16 rows, two column tiles a wavefront halve the activations' reads from LDS where
-  // enough workgroups remain (64 rows, 65536 x 7168: 103, 124 with one; 8192 x 7168: 24.7, 22.5)
+  // enough workgroups remain (64 rows, 65536 x 7168: 99, 124 with one; 8192 x 7168: 24.2, 22.0)
   p.nt = p.rows > 16 && n >= 16384 ? 2 : 1;
   // k divided over enough workgroups to fill the chip twice, each two slabs at least
   const int64_t tiles = ceil_div(n, 64 * p.nt) * ceil_div(rows, p.rows);

@@ -173,7 +173,8 @@ def nvfp4_kv_attention(q, cache, page_table, seq_lens, scale=None, prefix=None, 
     optional (prefix_table int32 [groups, pages], prefix_lens int32 [groups],
     group_offsets int32 [groups + 1]): sequences [group_offsets[g],
     group_offsets[g+1]) share prefix g in front of their own tokens; it is
-    read once for all of them.  scale: default 1/sqrt(head_dim).  lse=True
-    returns (out, log-sum-exp f32) as well."""
+    read and decoded once per 16 (groups of more than 256 query rows a cache
+    head: 32) of those rows.  scale: default 1/sqrt(head_dim).  head_dim 64,
+    128, 192 or 256.  lse=True returns (out, log-sum-exp f32) as well."""
     return (_ext or _native()).attention(q, cache, page_table, seq_lens, scale, prefix, lse, out,
                                          workspace)

@@ -36,7 +36,8 @@ extern "C" {
  *   codes         uint8 [n, k/2] ([num_groups, n, k/2] with groups), 8-byte
  *                 aligned; block_scales uint8 [.., n, k/16] (E4M3FN);
  *                 row_scales float [.., n], 4-byte aligned.
- *   rows          >= 0 (0: nothing is launched); n > 0; k > 0, a multiple of 16, up to 2^26.
+ *   rows          >= 0 (0: nothing is launched); n > 0; k > 0, a multiple of 16, up to 2^26;
+ *                 rows and n up to 2^30, and every tensor's elements up to 2^40.
  *   group_offsets NULL, or int64 [num_groups + 1] on the device, 8-byte
  *                 aligned, non-decreasing, within [0, rows]: the rows
  *                 [off[e], off[e+1]) are multiplied with expert e's matrix;
@@ -96,7 +97,7 @@ FP4Q_API int64_t mxfp4_linear_workspace_bytes(int64_t rows, int64_t n, int64_t k
  *             t * k_stride (v_stride): 16-byte aligned, strides multiples
  *             of 8 and at least kv_heads * head_dim (a slice of a fused
  *             projection is taken as it lies).
- *   tokens    >= 0.
+ *   tokens    >= 0, up to 2^30.
  *   slots     int64 [tokens] on the device, 8-byte aligned; a slot outside
  *             [0, num_pages * page_size) skips its token (padding: -1).  A
  *             slot given twice holds one of the tokens' rows or a mixture.
@@ -130,8 +131,16 @@ FP4Q_API fp4q_status nvfp4_kv_read(const uint8_t* k_codes, const uint8_t* k_scal
  * seq_lens[b] - q_tokens + 1 + i own tokens (none if that is below 1).
  * Query head h reads cache head h / (q_heads / kv_heads).  A query that
  * sees nothing gives zeros, and a log-sum-exp of -infinity.  Keys and values
- * are the exact g * e * s; scores and softmax sums are held in FP32, the
- * probabilities enter the value product in FP16.
+ * are the exact g * e * s; scores and softmax sums are held in FP32.  Queries
+ * enter in FP16 relative to their row's largest element (below 2^-39 of it
+ * they count as zero).  Weights, the probabilities times the values' token
+ * scales, enter the value product in FP16 relative to the query's largest:
+ * those below 2^-23 of it may be lost (where a batch's token scales lie more
+ * than 2^100 apart, or scores beyond 2^22, below 2^-23 of the largest scale).
+ * Scores up to 2^96 are told apart as FP32 does.  A query that sees a token
+ * whose value scale is infinite or NaN gives NaN; others are not touched by it.
+ * A NaN among the block scales (nvfp4_kv_append writes none) may reach the
+ * queries of its 64 tokens' group that do not see it.
  *
  *   q           BF16: query i of sequence b has its [q_heads, head_dim] rows
  *               at element (b * q_tokens + i) * q_stride; 16-byte aligned,
