@@ -73,15 +73,20 @@ def _current_stream(index):
     return torch.cuda.current_stream(index).cuda_stream
 
 
+def _native_module(name, path):
+    """A native half of the binding, loaded from the in-tree build."""
+    loader = importlib.machinery.ExtensionFileLoader(name, _open(path, name + ".so"))
+    spec = importlib.util.spec_from_file_location(name, path, loader=loader)
+    ext = importlib.util.module_from_spec(spec)
+    loader.exec_module(ext)
+    return ext
+
+
 def _native():
     """The native half of this binding, its calls bound to the library's."""
     global _ext
     if _ext is None:
-        path = _open(_build.ROLLOUT_EXT_PATH, "fp4q_rollout_ext.so")
-        loader = importlib.machinery.ExtensionFileLoader("fp4q_rollout_ext", path)
-        spec = importlib.util.spec_from_file_location("fp4q_rollout_ext", path, loader=loader)
-        ext = importlib.util.module_from_spec(spec)
-        loader.exec_module(ext)
+        ext = _native_module("fp4q_rollout_ext", _build.ROLLOUT_EXT_PATH)
         bind(ext, rollout_lib())
         _ext = ext
     return _ext
