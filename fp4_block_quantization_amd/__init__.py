@@ -22,7 +22,9 @@ Calls (same names as the C ABI):
 
 The operators that run on the quantized tensors (4-bit linear layers, the
 NVFP4 key/value cache and attention over it) are in rollout.py, C ABI in
-include/fp4q/rollout.h, and exported here under their names.
+include/fp4q/rollout.h, and exported here under their names; so are those that
+stand between them in a layer (rotary positions, attention over prompts,
+routing to experts: layer.py, include/fp4q/layer.h).
 """
 import ctypes
 import os
@@ -338,3 +340,9 @@ from .rollout import (NvFp4KvCache, mxfp4_linear, nvfp4_kv_append,  # noqa: E402
                       rollout_lib)
 
 __all__ += rollout.__all__
+
+from . import layer  # noqa: E402
+from .layer import (moe_combine, moe_dispatch, moe_route, prompt_attention,  # noqa: E402
+                    rotary, rotary_frequencies)
+
+__all__ += layer.__all__

@@ -26,17 +26,19 @@ STANDIN_PATH = os.path.join(BUILD_DIR, "libfp4q_standin.so")
 EXACTDECISION_PATH = os.path.join(BUILD_DIR, "libfp4q_exactdecision.so")
 # K0, the HBM probes (copy, read-only, write-only)
 MEMBENCH_PATH = os.path.join(BUILD_DIR, "libfp4q_membench.so")
-# the rollout engine's operators (include/fp4q/rollout.h)
+# the rollout engine's operators (include/fp4q/rollout.h and layer.h)
 ROLLOUT_PATH = os.path.join(BUILD_DIR, "libfp4q_rollout.so")
-# and the native half of their Python binding (host code only)
+# and the native halves of their Python binding (host code only)
 ROLLOUT_EXT_PATH = os.path.join(BUILD_DIR, "fp4q_rollout_ext.so")
+LAYER_EXT_PATH = os.path.join(BUILD_DIR, "fp4q_layer_ext.so")
 CSRC_ROLLOUT = os.path.join(HERE, "csrc_rollout")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["nvfp4.hip", "mxfp4_resq.hip", "fp4q_api.cpp"]
 MEMBENCH_SOURCES = ["membench.hip"]
 ROLLOUT_SOURCES = ["rollout_linear.hip", "rollout_cache.hip", "rollout_attention.hip",
-                   "rollout_api.cpp"]
+                   "rollout_api.cpp", "layer_rotary.hip", "layer_prompt.hip", "layer_route.hip",
+                   "layer_rows.hip", "layer_api.cpp"]
 
 HIP_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",
@@ -80,35 +82,44 @@ def build_rollout(verbose: bool = False) -> str:
     return build(verbose, out_path=ROLLOUT_PATH, sources=ROLLOUT_SOURCES, src_dir=CSRC_ROLLOUT)
 
 
-def build_rollout_ext(verbose: bool = False) -> str:
+def build_ext(source: str, out_path: str, verbose: bool = False) -> str:
+    """A native half of the rollout operators' binding."""
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension
     os.makedirs(BUILD_DIR, exist_ok=True)
-    tmp = ROLLOUT_EXT_PATH + ".tmp%d" % os.getpid()
+    tmp = out_path + ".tmp%d" % os.getpid()
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     includes = cpp_extension.include_paths() + [sysconfig.get_paths()["include"],
                                                 os.path.join(ROOT, "include")]
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
            *[a for i in includes for a in ("-isystem", i)],
-           os.path.join(CSRC_ROLLOUT, "rollout_ext.cpp"), "-L" + lib, "-ltorch_python",
+           os.path.join(CSRC_ROLLOUT, source), "-L" + lib, "-ltorch_python",
            "-ltorch_cpu", "-lc10", "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, ROLLOUT_EXT_PATH)
-    return ROLLOUT_EXT_PATH
+    os.replace(tmp, out_path)
+    return out_path
+
+
+def build_rollout_ext(verbose: bool = False) -> str:
+    return build_ext("rollout_ext.cpp", ROLLOUT_EXT_PATH, verbose)
+
+
+def build_layer_ext(verbose: bool = False) -> str:
+    return build_ext("layer_ext.cpp", LAYER_EXT_PATH, verbose)
 
 
 def build_all(verbose: bool = False):
     """libfp4q.so, its stand-in and exact-decision builds, the K0 probes,
-    libfp4q_rollout.so and its binding's native half."""
+    libfp4q_rollout.so and its binding's native halves."""
     return [build(verbose), build(verbose, ["-DFP4Q_STANDIN=1"], STANDIN_PATH),
             build(verbose, ["-DFP4Q_NV_CERTIFY=0"], EXACTDECISION_PATH),
             build(verbose, out_path=MEMBENCH_PATH, sources=MEMBENCH_SOURCES),
-            build_rollout(verbose), build_rollout_ext(verbose)]
+            build_rollout(verbose), build_rollout_ext(verbose), build_layer_ext(verbose)]
 
 
 if __name__ == "__main__":

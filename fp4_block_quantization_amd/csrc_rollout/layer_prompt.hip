@@ -1,0 +1,423 @@
+// layer_prompt.hip -- causal attention of packed sequences in BF16
+// (definition in include/fp4q/layer.h).
+//
+// Mathematics.  With c = |scale| log2(e) (queries take the scale's sign) and m
+// a row's running maximum of its scores s:
+//   p = 2^(s c - m c), l += p, O += p v;  out = O / l, lse = (m c + log2 l) ln 2
+// m is moved only when a score passes it by 8 / c: until then p is at most
+// 2^8, and BF16 holds that as well as 1.  p enters the value product in BF16
+// (8 bits, as the output has: a row's errors, 2^-9 each at most, are averaged
+// over its keys); s, m, l and O are FP32.  Where |m c| passes 2^20, s c - m c
+// is formed as (s - m) c, which does not cancel.
+//
+// Layout.  Scores are computed transposed, S^T = K Q^T (32 x 32 x 16 matrix
+// instructions): a lane holds 16 keys' scores of one query of every 32 keys,
+// so maxima and sums are its own but for one exchange between the halves of
+// the wavefront, and the probabilities of 16 keys, rounded to BF16, are the
+// operand of O^T = V^T P^T as they lie when the values' keys are taken in the
+// same order; the LDS's transposing read turns the values.  Keys and values go
+// to LDS without passing registers, 64 keys a step, two steps in flight, their
+// 16-byte pieces permuted within 128 bytes so that neither read has bank
+// conflicts.
+//
+// Work.  A workgroup takes the rows (query, head of those that share a key
+// head) of one sequence and key head, 32 a wavefront: the heads that share
+// keys share their loads as well, and few queries fill a tile.  Workgroup
+// numbers run over key heads first, so that a key head's workgroups meet in
+// the same dies' L2, and the last rows of a sequence, which see the most keys,
+// start first.
+#include "layer_launch.h"
+#include "rollout_divisor.h"
+
+namespace fp4q {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short short4v __attribute__((ext_vector_type(4)));
+typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+typedef float float16v __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr int kKeys = 64;  // of a step
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
+constexpr float kSlack = 8.0f;       // powers of two by which scores may pass m
+constexpr float kLarge = 0x1p20f;
+
+struct Params {
+  const uint16_t *q, *k, *v;
+  const int32_t *q_offsets, *k_offsets;
+  uint16_t* out;
+  float* lse;
+  int64_t q_stride, k_stride, v_stride;
+  int32_t q_tokens, k_tokens, q_heads, batch;
+  Divisor kv_heads;
+  Divisor per_head;  // query heads of a key head
+  int32_t blocks;    // of a key head: room for all sequences' row blocks
+  uint32_t first_block;
+  float c;           // |scale| log2(e)
+  uint32_t sign;     // 0x80008000 for a negative scale
+};
+
+// A sequence's rows and keys.
+struct Sequence {
+  int32_t q0, m, k0, n;
+};
+
+// Sequence b's row blocks are numbered from q_offsets[b] * per_head / RB + b on, which leaves room
+// for all of them: rows / RB, rounded up, is at most one more than the difference of that quotient.
+template <int RB>
+__device__ __forceinline__ int first_number(const Params& p, int b) {
+  const int32_t q0 = min(max(p.q_offsets[b], 0), p.q_tokens);
+  return (int)((uint32_t)q0 * p.per_head.d / RB) + b;
+}
+
+// The last sequence whose first number is at most w; 64 candidates at a time.
+template <int RB>
+__device__ __forceinline__ int sequence_of(const Params& p, int w) {
+  const int lane = threadIdx.x % 64;
+  int lo = 0, count = p.batch;  // it is one of [lo, lo + count); lo's number is at most w, or lo is 0
+  while (count > 1) {
+    const int step = (count + 63) / 64;
+    const int at = lo + lane * step;
+    const bool below = at < lo + count && first_number<RB>(p, at) <= w;
+    const uint64_t set = __ballot(below);
+    const int last = set == 0 ? 0 : 63 - __builtin_clzll(set);
+    count = min(step, lo + count - (lo + last * step));
+    lo += last * step;
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// 16 bytes a lane, from the lane's address to lds + 16 * lane.
+__device__ __forceinline__ void to_lds(const char* from, lds_void* lds) {
+  __builtin_amdgcn_global_load_lds(from, lds, 16, 0, 0);
+}
+
+__device__ __forceinline__ float other_half(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(threadIdx.x % 64 < 32 ? r[1] : r[0]);
+}
+
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// The order of a row's 16-byte pieces, exchanged within 8 of them: for eight neighbouring keys
+// all different, for four also without the lowest bit.
+__device__ __forceinline__ int turned(int key) { return (key & 3) << 1 | (key >> 2 & 1); }
+
+// Whether one of w's two BF16 numbers is infinite or NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+template <int D>
+struct Tile {
+  alignas(16) uint8_t k[kKeys * D * 2];
+  alignas(16) uint8_t v[kKeys * D * 2];
+};
+
+template <int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(const Params p) {
+  constexpr int RB = 32 * WAVES, NK = D / 16, DT = D / 32, kRow = 2 * D;
+  __shared__ Tile<D> tiles[2];
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int col = lane % 32, half = lane / 32;
+
+  const uint32_t id = p.first_block + blockIdx.x;
+  const uint32_t w_up = quotient(id, p.kv_heads);
+  const int kvh = (int)(id - w_up * p.kv_heads.d);
+  const int w = p.blocks - 1 - (int)w_up;
+  const int b = sequence_of<RB>(p, w);
+  Sequence s;
+  s.q0 = min(max(p.q_offsets[b], 0), p.q_tokens);
+  s.m = min(max(p.q_offsets[b + 1], s.q0), p.q_tokens) - s.q0;
+  s.k0 = min(max(p.k_offsets[b], 0), p.k_tokens);
+  s.n = min(max(p.k_offsets[b + 1], s.k0), p.k_tokens) - s.k0;
+  const int rows = (int)((uint32_t)s.m * p.per_head.d);
+  const int64_t row0 = ((int64_t)w - first_number<RB>(p, b)) * RB;
+  if (row0 < 0 || row0 >= rows) return;
+
+  // rows past the last are the last once more, and not stored
+  auto limit_of = [&](int r) {  // keys that row r sees
+    return max(0, s.n - s.m + 1 + (int)quotient((uint32_t)min(r, rows - 1), p.per_head));
+  };
+  const int first = (int)row0 + wave * 32, r = min(first + col, rows - 1);
+  const int token = (int)quotient((uint32_t)r, p.per_head);
+  const int head = kvh * (int)p.per_head.d + r - token * (int)p.per_head.d;
+  const int limit = limit_of(r);
+  const int block_limit = limit_of((int)row0 + RB - 1);
+  const int wave_limit = first < rows ? limit_of(first + 31) : 0;  // the most any row sees,
+  const int all_see = limit_of(first);                             // and the least
+  const int steps = (block_limit + kKeys - 1) / kKeys;
+
+  // queries, as the scores' second operand
+  bf16x8 q[NK];
+  {
+    const uint16_t* from = p.q + (int64_t)(s.q0 + token) * p.q_stride + head * D + half * 8;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      uint4v u = *(const uint4v*)(from + i * 16);
+      u ^= p.sign;
+      q[i] = __builtin_bit_cast(bf16x8, u);
+    }
+  }
+
+  // A step's copies: this wavefront's keys are the (64 / WAVES) from wave * 64 / WAVES on; the
+  // order of the pieces comes again every 8 keys, which are kPeriod copies.
+  constexpr int kPeriod = D / 64, kEights = 8 / WAVES;
+  const char* k_base = (const char*)(p.k + (int64_t)s.k0 * p.k_stride + kvh * D);
+  const char* v_base = (const char*)(p.v + (int64_t)s.k0 * p.v_stride + kvh * D);
+  const uint32_t k_row = (uint32_t)p.k_stride * 2, v_row = (uint32_t)p.v_stride * 2;  // bytes
+  auto piece_of = [&](int n, int& key, uint32_t& in_row) {  // of the n-th copy of eight keys
+    const int piece = n * 64 + lane;
+    key = piece / (D / 8);
+    in_row = (uint32_t)(piece % (D / 8) ^ turned(key)) * 16;
+  };
+  uint32_t k_from[kPeriod], v_from[kPeriod];
+#pragma unroll
+  for (int n = 0; n < kPeriod; ++n) {
+    int key;
+    uint32_t in_row;
+    piece_of(n, key, in_row);
+    k_from[n] = key * k_row + in_row;
+    v_from[n] = key * v_row + in_row;
+  }
+  auto copy = [&](int step) {
+    Tile<D>& t = tiles[step & 1];
+    const int key0 = step * kKeys + wave * kEights * 8;
+    if (step * kKeys + kKeys <= s.n) {
+#pragma unroll
+      for (int e = 0; e < kEights; ++e) {
+        const char* kb = k_base + (int64_t)(key0 + e * 8) * k_row;
+        const char* vb = v_base + (int64_t)(key0 + e * 8) * v_row;
+#pragma unroll
+        for (int n = 0; n < kPeriod; ++n) {
+          const int to = ((wave * kEights + e) * kPeriod + n) * 1024;
+          to_lds(kb + k_from[n], (lds_void*)(t.k + to));
+          to_lds(vb + v_from[n], (lds_void*)(t.v + to));
+        }
+      }
+    } else {
+      // keys past the sequence's end are its last once more
+#pragma unroll 1
+      for (int e = 0; e < kEights; ++e) {
+#pragma unroll 1
+        for (int n = 0; n < kPeriod; ++n) {
+          int key;
+          uint32_t in_row;
+          piece_of(n, key, in_row);
+          const int64_t from = min(key0 + e * 8 + key, s.n - 1);
+          const int to = ((wave * kEights + e) * kPeriod + n) * 1024;
+          to_lds(k_base + from * k_row + in_row, (lds_void*)(t.k + to));
+          to_lds(v_base + from * v_row + in_row, (lds_void*)(t.v + to));
+        }
+      }
+    }
+  };
+
+  float16v o[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i) o[i] = (float16v)0.0f;
+  float m = -INFINITY, mc = 0.0f, l = 0.0f;
+  bool large = false;
+
+  // where this lane's keys and values lie
+  int k_at[4], v_at[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) k_at[i] = col * kRow + ((2 * i + half) ^ turned(col)) * 16;
+  {
+    const int i = lane % 16, key = 4 * half + i / 4;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      v_at[j] = key * kRow + ((4 * j + 2 * (lane / 16 % 2) + i % 4 / 2) ^ turned(key)) * 16 +
+                i % 2 * 8;
+  }
+
+  auto step_of = [&](int step, bool masked) {
+    const Tile<D>& t = tiles[step & 1];
+    float16v sc[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      sc[kb] = (float16v)0.0f;
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        const bf16x8 a = *(const bf16x8*)(t.k + k_at[i % 4] + i / 4 * 128 + kb * 32 * kRow);
+        sc[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[i], sc[kb], 0, 0, 0);
+      }
+    }
+    const int seen = limit - step * kKeys - 4 * half;  // this lane's keys below that count
+    if (masked) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (kb * 32 + i / 4 * 8 + i % 4 >= seen) sc[kb][i] = -INFINITY;
+    }
+    float top = sc[0][0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) top = __builtin_fmaxf(top, sc[i / 16][i % 16]);
+    top = __builtin_fmaxf(top, other_half(top));
+    if (__any((top - m) * p.c > kSlack)) {
+      const float next = __builtin_fmaxf(m, top);
+      const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - next) * p.c);
+      m = next;
+      mc = m == -INFINITY ? 0.0f : m * p.c;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) o[i] *= f;
+      large = __any(__builtin_fabsf(mc) >= kLarge);
+    }
+    if (large) {
+      const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        sc[i / 16][i % 16] = __builtin_amdgcn_exp2f((sc[i / 16][i % 16] - base) * p.c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        sc[i / 16][i % 16] =
+            __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i / 16][i % 16], p.c, -mc));
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) l += sc[i / 16][i % 16];
+    uint4v weights[4];  // 16 keys each
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      weights[i / 4][i % 4] = pack(sc[i / 8][i % 8 * 2], sc[i / 8][i % 8 * 2 + 1]);
+    auto values = [&](int j, int d) {
+      uint4v a;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* at = t.v + v_at[d % 2] + d / 2 * 128 + (j * 16 + i * 8) * kRow;
+        const uint2v u = __builtin_bit_cast(
+            uint2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (__attribute__((address_space(3))) short4v*)at));
+        a[2 * i] = u[0];
+        a[2 * i + 1] = u[1];
+      }
+      return a;
+    };
+    if (masked) {
+      // A weight of zero does not take out an infinity or NaN: where the step has one, keys
+      // go one at a time to the rows that see them.
+      uint32_t bad = 0;
+#pragma unroll 4
+      for (int i = lane * 16; i < kKeys * kRow; i += 1024) {
+        const uint4v u = *(const uint4v*)(t.v + i);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) bad |= not_finite(u[x]);
+      }
+      if (__any(bad != 0)) {
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          const uint4v w = j == 0 ? weights[0] : j == 1 ? weights[1] : j == 2 ? weights[2]
+                                                                             : weights[3];
+#pragma unroll 1
+          for (int key = 0; key < 16; ++key) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              uint4v a = values(j, d);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                // these are keys 8 (i / 2) + 4 half + 2 (i % 2) and the next
+                const int at = key - (i / 2 * 8 + 4 * half + i % 2 * 2);
+                a[i] &= at == 0 ? 0xffffu : at == 1 ? 0xffff0000u : 0u;
+              }
+              float16v of = (float16v)0.0f;
+              of = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                           __builtin_bit_cast(bf16x8, w), of, 0,
+                                                           0, 0);
+              if (step * kKeys + j * 16 + key < limit) o[d] += of;
+            }
+          }
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            __builtin_bit_cast(bf16x8, values(j, d)), __builtin_bit_cast(bf16x8, weights[j]), o[d],
+            0, 0, 0);
+  };
+
+  if (steps > 0) copy(0);
+  for (int step = 0; step < steps; ++step) {
+    // this step's keys are there, and every wavefront is done with the tile that comes next
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (step + 1 < steps) copy(step + 1);
+    if (step * kKeys >= wave_limit) continue;
+    step_of(step, step * kKeys + kKeys > all_see);
+  }
+
+  l += other_half(l);
+  const float each = l == 0.0f ? 0.0f : 1.0f / l;
+  if (first + col < rows) {
+    const int64_t row = (int64_t)(s.q0 + token) * p.q_heads + head;
+    uint16_t* to = p.out + row * D + 4 * half;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint2v u = {pack(o[d][4 * i] * each, o[d][4 * i + 1] * each),
+                          pack(o[d][4 * i + 2] * each, o[d][4 * i + 3] * each)};
+        *(uint2v*)(to + d * 32 + i * 8) = u;
+      }
+    if (p.lse && half == 0)
+      p.lse[row] = l == 0.0f ? -INFINITY : (mc + __builtin_amdgcn_logf(l)) * kLn2;
+  }
+}
+
+}  // namespace
+
+int64_t prompt_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+
+hipError_t prompt_launch(const PromptArgs& a, hipStream_t stream) {
+  Params p{};
+  p.q = (const uint16_t*)a.q;
+  p.k = (const uint16_t*)a.k;
+  p.v = (const uint16_t*)a.v;
+  p.q_offsets = a.q_offsets;
+  p.k_offsets = a.k_offsets;
+  p.out = (uint16_t*)a.out;
+  p.lse = a.lse;
+  p.q_stride = a.q_stride;
+  p.k_stride = a.k_stride;
+  p.v_stride = a.v_stride;
+  p.q_tokens = (int32_t)a.q_tokens;
+  p.k_tokens = (int32_t)a.k_tokens;
+  p.q_heads = (int32_t)a.q_heads;
+  p.batch = (int32_t)a.batch;
+  p.kv_heads = divisor_of((uint32_t)a.kv_heads);
+  p.per_head = divisor_of((uint32_t)(a.q_heads / a.kv_heads));
+  const float c = __builtin_fabsf(a.scale) * kLog2e;
+  p.c = c > 0x1p-126f ? c : 0x1p-126f;  // (zero times an infinite score would be NaN)
+  p.sign = a.scale < 0.0f ? 0x80008000u : 0u;
+  constexpr int kWaves = 4;
+  p.blocks = (int32_t)(a.q_tokens * p.per_head.d / (32 * kWaves) + a.batch);
+  const int64_t total = (int64_t)p.blocks * a.kv_heads;
+  const int64_t most = ((int64_t)1 << 32) / (64 * kWaves) - 1;
+  for (int64_t first = 0; first < total; first += most) {
+    p.first_block = (uint32_t)first;
+    const uint32_t grid = (uint32_t)(total - first < most ? total - first : most);
+    const void* kernel = a.head_dim == 64    ? (void*)prompt_kernel<64, kWaves>
+                         : a.head_dim == 128 ? (void*)prompt_kernel<128, kWaves>
+                         : a.head_dim == 192 ? (void*)prompt_kernel<192, kWaves>
+                                             : (void*)prompt_kernel<256, kWaves>;
+    void* args[] = {&p};
+    const hipError_t e = hipLaunchKernel(kernel, dim3(grid), dim3(64 * kWaves), args, 0, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace fp4q

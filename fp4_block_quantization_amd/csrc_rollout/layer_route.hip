@@ -1,0 +1,312 @@
+// layer_route.hip -- scores of experts, the best of every token and their
+// weights (definition in include/fp4q/layer.h).
+//
+// Mathematics.  Keys become unsigned integers in the keys' order, so that the
+// largest of a wavefront is found with integer maxima.  Without a bias the
+// scores' order is the logits', and 32 bits hold it exactly.  A bias makes the
+// order depend on roundings of the scores: keys are FP64 then, so that two
+// experts change places only where their keys agree to 2^-52.  Groups' marks
+// are sums of two FP64 numbers for the same reason.
+//
+// Work.  One wavefront takes a token; a lane holds the experts lane, lane +
+// 64, and so on.  The best are taken one at a time: a maximum over the lane's
+// own, over the lanes (data-parallel moves, no LDS), and the lowest index of
+// those that are equal from ballots.
+#include "layer_launch.h"
+
+namespace fp4q {
+namespace {
+
+constexpr int kWaves = 4;
+
+struct Params {
+  const void* logits;
+  const float* bias;
+  const uint8_t* active;
+  float* weights;
+  int32_t* chosen;
+  int64_t tokens;
+  int32_t experts, top_k, groups, top_groups, per_group;
+  float scale;
+};
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
+}
+constexpr int kSwap1 = 0xb1, kSwap2 = 0x4e, kHalfMirror = 0x141, kMirror = 0x140;
+
+// Over all lanes, the same in every one.
+template <class T, class F>
+__device__ __forceinline__ T over_lanes(T v, F f) {
+  static_assert(sizeof(T) == 4 || sizeof(T) == 8, "one or two registers");
+  constexpr int W = sizeof(T) / 4;
+  auto step = [&](auto move) {
+    uint32_t w[W], m[W];
+    __builtin_memcpy(w, &v, sizeof(T));
+#pragma unroll
+    for (int i = 0; i < W; ++i) m[i] = move(w[i]);
+    T o;
+    __builtin_memcpy(&o, m, sizeof(T));
+    v = f(v, o);
+  };
+  step([](uint32_t x) { return moved<kSwap1>(x); });
+  step([](uint32_t x) { return moved<kSwap2>(x); });
+  step([](uint32_t x) { return moved<kHalfMirror>(x); });
+  step([](uint32_t x) { return moved<kMirror>(x); });
+  auto halves = [&](auto swap) {
+    uint32_t w[W], a[W], b[W];
+    __builtin_memcpy(w, &v, sizeof(T));
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const auto r = swap(w[i]);
+      a[i] = r[0];
+      b[i] = r[1];
+    }
+    T x, y;
+    __builtin_memcpy(&x, a, sizeof(T));
+    __builtin_memcpy(&y, b, sizeof(T));
+    v = f(x, y);
+  };
+  halves([](uint32_t x) { return __builtin_amdgcn_permlane16_swap(x, x, false, false); });
+  halves([](uint32_t x) { return __builtin_amdgcn_permlane32_swap(x, x, false, false); });
+  return v;
+}
+
+__device__ __forceinline__ uint32_t largest(uint32_t v) {
+  return over_lanes(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+
+// Ordered integers: 0 stands for "not there", 1 for NaN.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);  // (-0 counts as 0)
+  const uint32_t o = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return x != x ? 1u : o;
+}
+__device__ __forceinline__ uint64_t ordered(double x) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+  const uint64_t o = u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
+  return x != x ? 1ull : o;
+}
+
+// The place of the largest key: its slot and lane (of equal ones the lowest expert).
+template <int S, class K>
+__device__ __forceinline__ void best_of(const K (&key)[S], int& slot, int& lane) {
+  K own = key[0];
+#pragma unroll
+  for (int j = 1; j < S; ++j) own = key[j] > own ? key[j] : own;
+  K top;
+  if constexpr (sizeof(K) == 4) {
+    top = largest(own);
+  } else {
+    const uint32_t hi = largest((uint32_t)(own >> 32));
+    const uint32_t lo = (uint32_t)(own >> 32) == hi ? (uint32_t)own : 0u;
+    top = (uint64_t)hi << 32 | largest(lo);
+  }
+  slot = 0;
+  lane = 0;
+#pragma unroll
+  for (int j = S - 1; j >= 0; --j) {
+    const uint64_t with = __ballot(key[j] == top);
+    if (with != 0) {
+      slot = j;
+      lane = __builtin_ctzll(with);
+    }
+  }
+}
+
+// The two largest of some numbers.
+struct Two {
+  double first, second;
+  __device__ __forceinline__ void take(double v) {
+    const bool up = v > first;
+    second = up ? first : (v > second ? v : second);
+    first = up ? v : first;
+  }
+};
+
+__device__ __forceinline__ void own_lds_done() {  // a wavefront's LDS accesses are in order
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// S: experts of a lane.  WIDE: keys in FP64 (a bias, or groups).
+template <class T, int S, bool WIDE>
+__global__ __launch_bounds__(64 * kWaves) void route_kernel(const Params p, const bool sigmoid,
+                                                            const bool renormalize) {
+  using K = typename std::conditional<WIDE, uint64_t, uint32_t>::type;
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t token = (int64_t)blockIdx.x * kWaves + wave;
+  if (token >= p.tokens) return;
+  const int64_t at = token * p.top_k;
+  if (p.active && p.active[token] == 0) {
+    if (lane < p.top_k) {
+      p.weights[at + lane] = 0.0f;
+      p.chosen[at + lane] = -1;
+    }
+    return;
+  }
+  float x[S];
+  K key[S];
+  const T* row = (const T*)p.logits + token * p.experts;
+#pragma unroll
+  for (int j = 0; j < S; ++j) {
+    const int e = j * 64 + lane;
+    x[j] = e < p.experts ? (float)row[e] : -INFINITY;
+  }
+  float top = x[0];
+#pragma unroll
+  for (int j = 1; j < S; ++j) top = __builtin_fmaxf(top, x[j]);
+  top = over_lanes(top, [](float a, float b) { return __builtin_fmaxf(a, b); });
+  if constexpr (WIDE) {
+    double score[S];
+    if (sigmoid) {
+#pragma unroll
+      for (int j = 0; j < S; ++j) score[j] = 1.0 / (1.0 + exp(-(double)x[j]));
+    } else {
+      double sum = 0.0;
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        // (a row of -infinity only has no scores: zeros)
+        score[j] = top == -INFINITY ? 0.0 : exp((double)x[j] - (double)top);
+        sum += score[j];
+      }
+      sum = over_lanes(sum, [](double a, double b) { return a + b; });
+      const double each = sum == 0.0 ? 0.0 : 1.0 / sum;
+#pragma unroll
+      for (int j = 0; j < S; ++j) score[j] *= each;
+    }
+    double mark[S];
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      const int e = j * 64 + lane;
+      if (p.bias) {
+        mark[j] = score[j] + (double)p.bias[e < p.experts ? e : 0];
+        key[j] = ordered(mark[j]);
+      } else {
+        mark[j] = score[j];
+        key[j] = (uint64_t)ordered(x[j]) << 32;
+      }
+      if (e >= p.experts) key[j] = 0;
+    }
+    if (p.groups > 1) {
+      __shared__ double marks[kWaves][S * 64];
+#pragma unroll
+      for (int j = 0; j < S; ++j) marks[wave][j * 64 + lane] = mark[j];
+      own_lds_done();
+      // `share` lanes a group, a power of two
+      int share = 64;
+      while (share * p.groups > 64) share /= 2;
+      const int g = lane / share;
+      Two two{-INFINITY, -INFINITY};
+      if (g < p.groups)
+        for (int i = lane % share; i < p.per_group; i += share)
+          two.take(marks[wave][g * p.per_group + i]);
+      for (int s = 1; s < share; s *= 2) {
+        const double a = __shfl_xor(two.first, s), b = __shfl_xor(two.second, s);
+        two.take(a);
+        two.take(b);
+      }
+      // (groups of one expert have no second)
+      const double sum = p.per_group > 1 ? two.first + two.second : two.first;
+      const uint64_t own = g < p.groups ? ordered(sum) : 0;
+      int ahead = 0;  // groups that come before this lane's
+      for (int i = 0; i < p.groups; ++i) {
+        const uint64_t other = __shfl(own, i * share);
+        ahead += other > own || (other == own && i < g);
+      }
+      const uint64_t open = __ballot(ahead < p.top_groups && g < p.groups);
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        const int of = (j * 64 + lane) / p.per_group;
+        if (of < p.groups && !(open >> (of * share) & 1)) key[j] = 0;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < S; ++j) key[j] = j * 64 + lane < p.experts ? ordered(x[j]) : 0u;
+  }
+  float logit = 0.0f;  // of the lane-th choice
+  int expert = 0;
+  for (int i = 0; i < p.top_k; ++i) {
+    int slot, from;
+    best_of<S, K>(key, slot, from);
+    float v = 0.0f;
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      if (slot == j) {
+        v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x[j]), from));
+        if (lane == from) key[j] = 0;
+      }
+    }
+    if (lane == i) {
+      logit = v;
+      expert = slot * 64 + from;
+    }
+  }
+  float w = 0.0f;
+  auto add = [](float a, float b) { return a + b; };
+  if (sigmoid) {
+    if (lane < p.top_k) w = 1.0f / (1.0f + expf(-logit));
+    if (renormalize) {
+      const float sum = over_lanes(w, add);
+      w = sum == 0.0f ? 0.0f : w / sum;
+    }
+  } else if (renormalize) {
+    // relative to the largest chosen: what the others add to the sum cancels
+    const float most = over_lanes(lane < p.top_k ? logit : -INFINITY,
+                                  [](float a, float b) { return __builtin_fmaxf(a, b); });
+    if (lane < p.top_k && most != -INFINITY) w = expf(logit - most);
+    const float sum = over_lanes(w, add);
+    w = sum == 0.0f ? 0.0f : w / sum;
+  } else {
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < S; ++j) sum += top == -INFINITY ? 0.0f : expf(x[j] - top);
+    sum = over_lanes(sum, add);
+    if (lane < p.top_k && top != -INFINITY) w = expf(logit - top) / sum;
+  }
+  if (lane < p.top_k) {
+    p.weights[at + lane] = w * p.scale;
+    p.chosen[at + lane] = expert;
+  }
+}
+
+template <class T, bool WIDE>
+void* kernel_of(int64_t experts) {
+  const int64_t s = (experts + 63) / 64;
+  if (s <= 1) return (void*)route_kernel<T, 1, WIDE>;
+  if (s <= 2) return (void*)route_kernel<T, 2, WIDE>;
+  if (s <= 4) return (void*)route_kernel<T, 4, WIDE>;
+  if (s <= 8) return (void*)route_kernel<T, 8, WIDE>;
+  return (void*)route_kernel<T, 16, WIDE>;
+}
+
+}  // namespace
+
+hipError_t route_launch(const RouteArgs& a, hipStream_t stream) {
+  Params p{a.logits, a.bias, a.active, a.weights, a.chosen, a.tokens, (int32_t)a.experts,
+           (int32_t)a.top_k, (int32_t)a.groups, (int32_t)a.top_groups,
+           (int32_t)(a.experts / a.groups), a.scale};
+  const bool wide = a.bias || a.groups > 1;
+  void* kernel = a.fp32 ? (wide ? kernel_of<float, true>(a.experts) : kernel_of<float, false>(a.experts))
+                        : (wide ? kernel_of<__bf16, true>(a.experts)
+                                : kernel_of<__bf16, false>(a.experts));
+  bool sigmoid = a.sigmoid, renormalize = a.renormalize;
+  // (a launch holds 2^32 threads)
+  const int64_t step = (int64_t)kWaves << 23;
+  for (int64_t first = 0; first < a.tokens; first += step) {
+    p.tokens = a.tokens - first < step ? a.tokens - first : step;
+    void* args[] = {&p, &sigmoid, &renormalize};
+    const hipError_t e = hipLaunchKernel(kernel, dim3((uint32_t)((p.tokens + kWaves - 1) / kWaves)),
+                                         dim3(64 * kWaves), args, 0, stream);
+    if (e != hipSuccess) return e;
+    p.logits = (const char*)p.logits + p.tokens * p.experts * (a.fp32 ? 4 : 2);
+    if (p.active) p.active += p.tokens;
+    p.weights += p.tokens * p.top_k;
+    p.chosen += p.tokens * p.top_k;
+  }
+  return hipSuccess;
+}
+
+}  // namespace fp4q

@@ -1,0 +1,356 @@
+// layer_rows.hip -- tokens' rows to their experts' places, and the weighted
+// sums back (definitions in include/fp4q/layer.h).
+//
+// Mathematics.  A stable counting sort of the tokens * top_k choices by
+// expert: a choice's place is the number of choices of lower experts, plus
+// those of the same expert before it.  Whole numbers throughout, so the order
+// of additions does not matter; places are the same from call to call.
+//
+// Work.  Few choices: every workgroup counts them all and copies its token's
+// row, one launch.  Many: counts per chunk of choices; places from the counts
+// of the chunks before; then the rows, each token's read once and written to
+// its places.  The sums back read every row once.  Both are bounded by memory
+// once there are a few thousand rows, by the launches below.
+#include "layer_launch.h"
+#include "rollout_divisor.h"
+
+namespace fp4q {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kChunk = 2048;       // choices of a workgroup that counts or places
+constexpr int64_t kFew = 4096;     // choices up to which one launch does everything
+constexpr int kMaxExperts = 1024, kMaxChoices = 64;
+
+struct Params {
+  const char* x;
+  char* rows;
+  const int32_t* chosen;
+  int64_t* offsets;
+  int32_t* place;
+  int32_t* counts;  // [chunks][experts]
+  int64_t hidden;
+  Divisor top_k;
+  int32_t entries, experts, chunks;
+  int64_t tokens;
+};
+
+// counts[e] -> their sums before e, for threads of one workgroup; the sum of all is returned.
+__device__ __forceinline__ int scan_counts(int* counts, int experts, int (&shared)[kWaves]) {
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int each = (experts + kThreads - 1) / kThreads;
+  const int lo = min(tid * each, experts), hi = min(lo + each, experts);
+  int own = 0;
+  for (int e = lo; e < hi; ++e) own += counts[e];
+  int upto = own;
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) {
+    const int o = __shfl_up(upto, s);
+    if (lane >= s) upto += o;
+  }
+  if (lane == 63) shared[wave] = upto;
+  __syncthreads();
+  int before = upto - own, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) before += shared[w];
+    all += shared[w];
+  }
+  for (int e = lo; e < hi; ++e) {
+    const int n = counts[e];
+    counts[e] = before;
+    before += n;
+  }
+  __syncthreads();
+  return all;
+}
+
+// V bytes at a time from a token's row to the places of its choices.
+template <class V>
+__device__ __forceinline__ void copy_row(const Params& p, int64_t token, const int* place, int first,
+                                         int step) {
+  const int64_t bytes = p.hidden * 2, pieces = bytes / (int64_t)sizeof(V);
+  const V* from = (const V*)(p.x + token * bytes);
+  for (int64_t i = first; i < pieces; i += step) {
+    const V v = from[i];
+    for (int j = 0; j < (int)p.top_k.d; ++j)
+      if (place[j] >= 0) ((V*)(p.rows + (int64_t)place[j] * bytes))[i] = v;
+  }
+}
+
+// One workgroup a token and part of its row; every one counts all choices.
+template <class V>
+__global__ __launch_bounds__(kThreads) void dispatch_few(const Params p) {
+  __shared__ int total[kMaxExperts], before[kMaxExperts], sums[kWaves], places[kMaxChoices];
+  const int tid = threadIdx.x, k = (int)p.top_k.d;
+  for (int e = tid; e < p.experts; e += kThreads) total[e] = before[e] = 0;
+  __syncthreads();
+  const int own = blockIdx.x * k;  // the token's first choice
+  for (int i = tid; i < p.entries; i += kThreads) {
+    const int e = p.chosen[i];
+    if ((uint32_t)e >= (uint32_t)p.experts) continue;
+    atomicAdd(&total[e], 1);
+    if (i < own) atomicAdd(&before[e], 1);
+  }
+  __syncthreads();
+  const int all = scan_counts(total, p.experts, sums);
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    for (int e = tid; e < p.experts; e += kThreads) p.offsets[e] = total[e];
+    if (tid == 0) p.offsets[p.experts] = all;
+  }
+  if (p.entries == 0) return;
+  if (tid < k) {
+    const int e = p.chosen[own + tid];
+    int at = -1;
+    if ((uint32_t)e < (uint32_t)p.experts) {
+      at = total[e] + before[e];
+      for (int j = 0; j < tid; ++j) at += p.chosen[own + j] == e;
+    }
+    places[tid] = at;
+    if (blockIdx.y == 0) p.place[own + tid] = at;
+  }
+  __syncthreads();
+  copy_row<V>(p, blockIdx.x, places, blockIdx.y * kThreads + tid, gridDim.y * kThreads);
+}
+
+__global__ __launch_bounds__(kThreads) void count_chunks(const Params p) {
+  __shared__ int count[kMaxExperts];
+  const int tid = threadIdx.x;
+  for (int e = tid; e < p.experts; e += kThreads) count[e] = 0;
+  __syncthreads();
+  const int lo = blockIdx.x * kChunk, hi = min(lo + kChunk, p.entries);
+  for (int i = lo + tid; i < hi; i += kThreads) {
+    const int e = p.chosen[i];
+    if ((uint32_t)e < (uint32_t)p.experts) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  for (int e = tid; e < p.experts; e += kThreads)
+    p.counts[(int64_t)blockIdx.x * p.experts + e] = count[e];
+}
+
+// Places of a chunk's choices.  A wavefront takes a quarter of them, 64 at a time in order;
+// next[wave][e] is the place of the next choice of e that the wavefront meets.
+__global__ __launch_bounds__(kThreads) void place_chunks(const Params p) {
+  __shared__ int base[kMaxExperts], next[kWaves][kMaxExperts], sums[kWaves];
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, chunk = blockIdx.x;
+  int mine[kMaxExperts / kThreads];  // of the experts tid, tid + kThreads, ..: in chunks before
+#pragma unroll
+  for (int j = 0; j < kMaxExperts / kThreads; ++j) {
+    const int e = j * kThreads + tid;
+    mine[j] = 0;
+    if (e >= p.experts) continue;
+    int all = 0, before = 0;
+#pragma unroll 8
+    for (int c = 0; c < p.chunks; ++c) {
+      const int n = p.counts[(int64_t)c * p.experts + e];
+      all += n;
+      before += c < chunk ? n : 0;
+    }
+    base[e] = all;
+    mine[j] = before;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) next[w][e] = 0;
+  }
+  __syncthreads();
+  const int all = scan_counts(base, p.experts, sums);
+  if (chunk == 0) {
+    for (int e = tid; e < p.experts; e += kThreads) p.offsets[e] = base[e];
+    if (tid == 0) p.offsets[p.experts] = all;
+  }
+  constexpr int kShare = kChunk / kWaves, kRounds = kShare / 64;
+  const int lo = chunk * kChunk + wave * kShare;
+  int own[kRounds];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int i = lo + r * 64 + lane;
+    own[r] = i < p.entries ? p.chosen[i] : -1;
+    if ((uint32_t)own[r] >= (uint32_t)p.experts) own[r] = -1;
+    if (own[r] >= 0) atomicAdd(&next[wave][own[r]], 1);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kMaxExperts / kThreads; ++j) {
+    const int e = j * kThreads + tid;
+    if (e >= p.experts) continue;
+    int at = base[e] + mine[j];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const int n = next[w][e];
+      next[w][e] = at;
+      at += n;
+    }
+  }
+  __syncthreads();
+  const int bits = 32 - __builtin_clz(p.experts);  // experts, and one number for none
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int i = lo + r * 64 + lane;
+    const int e = own[r] >= 0 ? own[r] : p.experts;
+    uint64_t peers = ~0ull;  // lanes with the same expert
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = __ballot((e >> b) & 1);
+      peers &= (e >> b) & 1 ? set : ~set;
+    }
+    int at = -1;
+    if (own[r] >= 0) {
+      const int ahead = __popcll(peers & ((1ull << lane) - 1));
+      at = next[wave][e] + ahead;
+    }
+    // every lane has read its expert's number before the first of them moves it on
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (own[r] >= 0 && (peers >> lane) == 1) next[wave][e] = at + 1;  // (the last of them)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (i < p.entries) p.place[i] = at;
+  }
+}
+
+// A wavefront a token at a time.
+template <class V>
+__global__ __launch_bounds__(kThreads) void copy_rows(const Params p) {
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < p.tokens;
+       t += (int64_t)gridDim.x * kWaves)
+    copy_row<V>(p, t, p.place + t * p.top_k.d, lane, 64);
+}
+
+struct Sums {
+  const char* y;
+  const int32_t* place;
+  const float* weights;
+  const char* add;
+  char* out;
+  int64_t tokens, n, y_rows;
+  int32_t top_k;
+};
+
+template <class T, int N>
+__device__ __forceinline__ void load_run(const char* base, int64_t at, float (&v)[N]) {
+  if constexpr (N == 1) {
+    v[0] = (float)((const T*)base)[at];
+  } else {
+    // 16 bytes at a time
+    constexpr int E = 16 / sizeof(T);
+    typedef T vec __attribute__((ext_vector_type(E)));
+#pragma unroll
+    for (int i = 0; i < N / E; ++i) {
+      const vec w = *(const vec*)((const T*)base + at + i * E);
+#pragma unroll
+      for (int j = 0; j < E; ++j) v[i * E + j] = (float)w[j];
+    }
+  }
+}
+
+template <class T, int N>
+__device__ __forceinline__ void store_run(char* base, int64_t at, const float (&v)[N]) {
+  if constexpr (N == 1) {
+    ((T*)base)[at] = (T)v[0];
+  } else {
+    constexpr int E = 16 / sizeof(T);
+    typedef T vec __attribute__((ext_vector_type(E)));
+#pragma unroll
+    for (int i = 0; i < N / E; ++i) {
+      vec w;
+#pragma unroll
+      for (int j = 0; j < E; ++j) w[j] = (T)v[i * E + j];
+      *(vec*)((T*)base + at + i * E) = w;
+    }
+  }
+}
+
+// A workgroup takes a token and a part of its columns; a thread N of them.
+template <class T, class O, int N>
+__global__ __launch_bounds__(kThreads) void combine_kernel(const Sums p) {
+  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+    const int32_t* place = p.place + t * p.top_k;
+    const float* weights = p.weights + t * p.top_k;
+    for (int64_t c = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * N; c < p.n;
+         c += (int64_t)gridDim.y * kThreads * N) {
+      float sum[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum[i] = 0.0f;
+      if (p.add) load_run<__bf16, N>(p.add, t * p.n + c, sum);
+#pragma unroll 4
+      for (int j = 0; j < p.top_k; ++j) {
+        const int at = place[j];
+        if (at < 0 || at >= p.y_rows) continue;
+        const float w = weights[j];
+        float v[N];
+        load_run<T, N>(p.y, at * p.n + c, v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum[i] = __builtin_fmaf(w, v[i], sum[i]);
+      }
+      store_run<O, N>(p.out, t * p.n + c, sum);
+    }
+  }
+}
+
+}  // namespace
+
+int64_t dispatch_workspace_bytes(int64_t tokens, int64_t top_k, int64_t experts) {
+  const int64_t entries = tokens * top_k;
+  return entries <= kFew ? 0 : (entries + kChunk - 1) / kChunk * experts * 4;
+}
+
+hipError_t dispatch_launch(const DispatchArgs& a, hipStream_t stream) {
+  Params p{};
+  p.x = (const char*)a.x;
+  p.rows = (char*)a.rows;
+  p.chosen = a.chosen;
+  p.offsets = a.offsets;
+  p.place = a.place;
+  p.counts = (int32_t*)a.workspace;
+  p.hidden = a.hidden;
+  p.top_k = divisor_of((uint32_t)a.top_k);
+  p.entries = (int32_t)(a.tokens * a.top_k);
+  p.experts = (int32_t)a.experts;
+  p.chunks = (int32_t)(((int64_t)p.entries + kChunk - 1) / kChunk);
+  p.tokens = a.tokens;
+  const bool wide = a.hidden % 8 == 0 && ((uintptr_t)a.x | (uintptr_t)a.rows) % 16 == 0;
+  const int64_t pieces = wide ? a.hidden / 8 : a.hidden;
+  if (p.entries <= kFew) {
+    // workgroups for the chip's 256 compute units, of a piece a thread at least
+    const int64_t want = a.tokens > 0 ? (512 + a.tokens - 1) / a.tokens : 1;
+    const int64_t most = (pieces + kThreads - 1) / kThreads;
+    const dim3 grid((uint32_t)(a.tokens > 0 ? a.tokens : 1), (uint32_t)(want < most ? want : most));
+    if (wide)
+      dispatch_few<uint4><<<grid, kThreads, 0, stream>>>(p);
+    else
+      dispatch_few<uint16_t><<<grid, kThreads, 0, stream>>>(p);
+    return hipGetLastError();
+  }
+  count_chunks<<<p.chunks, kThreads, 0, stream>>>(p);
+  place_chunks<<<p.chunks, kThreads, 0, stream>>>(p);
+  const int64_t blocks = (a.tokens + kWaves - 1) / kWaves;
+  const uint32_t grid = (uint32_t)(blocks < (1 << 20) ? blocks : (1 << 20));
+  if (wide)
+    copy_rows<uint4><<<grid, kThreads, 0, stream>>>(p);
+  else
+    copy_rows<uint16_t><<<grid, kThreads, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t combine_launch(const CombineArgs& a, hipStream_t stream) {
+  const Sums p{(const char*)a.y, a.place, a.weights, (const char*)a.add, (char*)a.out, a.tokens,
+               a.n,              a.y_rows, (int32_t)a.top_k};
+  const bool wide = a.n % 8 == 0 &&
+                    ((uintptr_t)a.y | (uintptr_t)a.out | (uintptr_t)a.add) % 16 == 0;
+  const int64_t parts = (a.n / (wide ? 8 : 1) + kThreads - 1) / kThreads;
+  const dim3 grid((uint32_t)(a.tokens < (1 << 20) ? a.tokens : (1 << 20)),
+                  (uint32_t)(parts < 1 ? 1 : parts < 8 ? parts : 8));
+  auto go = [&](auto t, auto o) {
+    using T = decltype(t);
+    using O = decltype(o);
+    if (wide)
+      combine_kernel<T, O, 8><<<grid, kThreads, 0, stream>>>(p);
+    else
+      combine_kernel<T, O, 1><<<grid, kThreads, 0, stream>>>(p);
+    return hipGetLastError();
+  };
+  if (a.y_fp32) return a.out_fp32 ? go(0.0f, 0.0f) : go(0.0f, __bf16{});
+  return a.out_fp32 ? go(__bf16{}, 0.0f) : go(__bf16{}, __bf16{});
+}
+
+}  // namespace fp4q
