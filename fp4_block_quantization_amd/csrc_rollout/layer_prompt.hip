@@ -111,9 +111,10 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 // all different, for four also without the lowest bit.
 __device__ __forceinline__ int turned(int key) { return (key & 3) << 1 | (key >> 2 & 1); }
 
-// Whether one of w's two BF16 numbers is infinite or NaN.
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+// Two BF16 numbers with zeros for infinities and NaN.
+__device__ __forceinline__ uint32_t finite_part(uint32_t w) {
+  return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) |
+         ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
 }
 
 template <int D>
@@ -225,7 +226,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
 #pragma unroll
   for (int i = 0; i < DT; ++i) o[i] = (float16v)0.0f;
   float m = -INFINITY, mc = 0.0f, l = 0.0f;
-  bool large = false;
+  bool large = false, any_dirty = false;
 
   // where this lane's keys and values lie
   int k_at[4], v_at[2];
@@ -303,50 +304,40 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
       }
       return a;
     };
+    auto product = [&](auto clean) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          uint4v a = values(j, d);
+          if constexpr (decltype(clean)::value) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = finite_part(a[i]);
+          }
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                         __builtin_bit_cast(bf16x8, weights[j]),
+                                                         o[d], 0, 0, 0);
+        }
+    };
+    // A weight of zero does not take out an infinity or NaN: where a step that not every row sees
+    // whole has one, it is left out here and added behind the loop.
+    bool dirty = false;
     if (masked) {
-      // A weight of zero does not take out an infinity or NaN: where the step has one, keys
-      // go one at a time to the rows that see them.
       uint32_t bad = 0;
 #pragma unroll 4
       for (int i = lane * 16; i < kKeys * kRow; i += 1024) {
         const uint4v u = *(const uint4v*)(t.v + i);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) bad |= not_finite(u[x]);
+        for (int x = 0; x < 4; ++x) bad |= finite_part(u[x]) ^ u[x];
       }
-      if (__any(bad != 0)) {
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          const uint4v w = j == 0 ? weights[0] : j == 1 ? weights[1] : j == 2 ? weights[2]
-                                                                             : weights[3];
-#pragma unroll 1
-          for (int key = 0; key < 16; ++key) {
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              uint4v a = values(j, d);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                // these are keys 8 (i / 2) + 4 half + 2 (i % 2) and the next
-                const int at = key - (i / 2 * 8 + 4 * half + i % 2 * 2);
-                a[i] &= at == 0 ? 0xffffu : at == 1 ? 0xffff0000u : 0u;
-              }
-              float16v of = (float16v)0.0f;
-              of = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
-                                                           __builtin_bit_cast(bf16x8, w), of, 0,
-                                                           0, 0);
-              if (step * kKeys + j * 16 + key < limit) o[d] += of;
-            }
-          }
-        }
-        return;
-      }
+      dirty = __any(bad != 0);
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            __builtin_bit_cast(bf16x8, values(j, d)), __builtin_bit_cast(bf16x8, weights[j]), o[d],
-            0, 0, 0);
+    if (dirty) {
+      any_dirty = true;
+      product(std::true_type{});
+    } else {
+      product(std::false_type{});
+    }
   };
 
   if (steps > 0) copy(0);
@@ -357,6 +348,26 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
     if (step + 1 < steps) copy(step + 1);
     if (step * kKeys >= wave_limit) continue;
     step_of(step, step * kKeys + kKeys > all_see);
+  }
+
+  if (any_dirty) {
+    // values that are not finite, of the steps that were masked, to the rows that see them
+    const char* from = v_base + (int64_t)(all_see / kKeys * kKeys) * v_row + 8 * half;
+#pragma unroll 1
+    for (int key = all_see / kKeys * kKeys; key < wave_limit; ++key, from += v_row) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint2v u = *(const uint2v*)(from + d * 64 + i * 16);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t bits = x % 2 ? u[x / 2] & 0xffff0000u : u[x / 2] << 16;
+            if ((bits & 0x7f800000u) == 0x7f800000u && key < limit)
+              o[d][4 * i + x] += __uint_as_float(bits);
+          }
+        }
+    }
   }
 
   l += other_half(l);

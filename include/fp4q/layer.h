@@ -70,7 +70,8 @@ FP4Q_API fp4q_status rotary_embed(const void* q, int64_t q_stride, int64_t q_hea
  * are.  Scores, maxima, sums and outputs are held in FP32; probabilities
  * enter the value product in BF16, relative to the row's largest (up to 2^8
  * of an earlier largest).  Keys and values that a query does not see have no
- * effect on it, infinities and NaN among them.
+ * effect on it, infinities and NaN among them; a value that is not finite, where
+ * a query sees it, makes that element of its output infinite or NaN.
  *
  *   q            BF16: token t's [q_heads, head_dim] rows at element t * q_stride.
  *   k, v         BF16 [.., kv_heads, head_dim] rows likewise.  16-byte aligned,

@@ -233,14 +233,14 @@ def test_infinite_values_behind_the_last_key():
 
 
 def test_a_value_without_weight():
-    # seen with a weight that underflows: 0 times infinity, as the formula has it
+    # seen with a weight that underflows: infinite, or NaN as 0 times infinity is
     n, d = 80, 64
     q, k, v = torch.ones((n, 1, d)), torch.zeros((n, 1, d)), tensor(n, 1, d, seed=33)
     k[3] = -100.0
     q, k = q.cuda().bfloat16(), k.cuda().bfloat16()
     v[3, 0, 7] = math.inf
     out = fq.prompt_attention(q, k, v, offsets([n])).float()
-    assert torch.isnan(out[4:, 0, 7]).all() and torch.isfinite(out[:3]).all()
+    assert not torch.isfinite(out[3:, 0, 7]).any() and torch.isfinite(out[:3]).all()
     rest = [i for i in range(d) if i != 7]
     assert torch.isfinite(out[:, 0, rest]).all()
 
