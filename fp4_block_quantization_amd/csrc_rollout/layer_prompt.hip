@@ -90,9 +90,17 @@ __device__ __forceinline__ int sequence_of(const Params& p, int w) {
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// 16 bytes a lane, from the lane's address to lds + 16 * lane.
-__device__ __forceinline__ void to_lds(const char* from, lds_void* lds) {
-  __builtin_amdgcn_global_load_lds(from, lds, 16, 0, 0);
+// 16 bytes a lane, from base + scalar + lane's offset to lds + 16 * lane.  (Written out: the
+// compiler would wait for all copies in flight before the next transposing read, whatever it
+// reads.  Nothing is returned to registers; the callers wait for vmcnt before the tiles are read.
+// m0 holds nothing of the compiler's here.)
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t base, uint32_t lane, uint32_t scalar,
+                                       uint8_t* lds) {
+  const uint32_t at = (uint32_t)(uintptr_t)(lds_void*)lds;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(at), "v"(lane), "s"(base), "s"(scalar)
+               : "memory");
 }
 
 __device__ __forceinline__ float other_half(float x) {
@@ -118,15 +126,15 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t w) {
 }
 
 template <int D>
-struct Tile {
-  alignas(16) uint8_t k[kKeys * D * 2];
-  alignas(16) uint8_t v[kKeys * D * 2];
+struct Tiles {
+  alignas(16) uint8_t k[2][kKeys * D * 2];
+  alignas(16) uint8_t v[2][kKeys * D * 2];
 };
 
 template <int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(const Params p) {
   constexpr int RB = 32 * WAVES, NK = D / 16, DT = D / 32, kRow = 2 * D;
-  __shared__ Tile<D> tiles[2];
+  __shared__ Tiles<D> tiles;
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int col = lane % 32, half = lane / 32;
 
@@ -189,21 +197,19 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
     k_from[n] = key * k_row + in_row;
     v_from[n] = key * v_row + in_row;
   }
-  auto copy = [&](int step) {
-    Tile<D>& t = tiles[step & 1];
-    const int key0 = step * kKeys + wave * kEights * 8;
+  // a step's keys (or values) to tile step % 2
+  auto copy = [&](int step, const char* base, uint32_t row, const uint32_t (&from)[kPeriod],
+                  uint8_t (&tile)[2][kKeys * D * 2]) {
+    uint8_t* t = tile[step & 1] + wave * kEights * kPeriod * 1024;
+    const auto at = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(base + (int64_t)step * kKeys * row), 0, -1, 0x20000);
+    const uint32_t key0 = wave * kEights * 8;
     if (step * kKeys + kKeys <= s.n) {
 #pragma unroll
-      for (int e = 0; e < kEights; ++e) {
-        const char* kb = k_base + (int64_t)(key0 + e * 8) * k_row;
-        const char* vb = v_base + (int64_t)(key0 + e * 8) * v_row;
+      for (int e = 0; e < kEights; ++e)
 #pragma unroll
-        for (int n = 0; n < kPeriod; ++n) {
-          const int to = ((wave * kEights + e) * kPeriod + n) * 1024;
-          to_lds(kb + k_from[n], (lds_void*)(t.k + to));
-          to_lds(vb + v_from[n], (lds_void*)(t.v + to));
-        }
-      }
+        for (int n = 0; n < kPeriod; ++n)
+          to_lds(at, from[n], (key0 + e * 8) * row, t + (e * kPeriod + n) * 1024);
     } else {
       // keys past the sequence's end are its last once more
 #pragma unroll 1
@@ -213,13 +219,17 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
           int key;
           uint32_t in_row;
           piece_of(n, key, in_row);
-          const int64_t from = min(key0 + e * 8 + key, s.n - 1);
-          const int to = ((wave * kEights + e) * kPeriod + n) * 1024;
-          to_lds(k_base + from * k_row + in_row, (lds_void*)(t.k + to));
-          to_lds(v_base + from * v_row + in_row, (lds_void*)(t.v + to));
+          const uint32_t k = min((int)key0 + e * 8 + key, s.n - 1 - step * kKeys);
+          to_lds(at, k * row + in_row, 0, t + (e * kPeriod + n) * 1024);
         }
       }
     }
+  };
+  auto copy_keys = [&](int step) {
+    if (step < steps) copy(step, k_base, k_row, k_from, tiles.k);
+  };
+  auto copy_values = [&](int step) {
+    if (step < steps) copy(step, v_base, v_row, v_from, tiles.v);
   };
 
   float16v o[DT];
@@ -240,29 +250,26 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
                 i % 2 * 8;
   }
 
-  auto step_of = [&](int step, bool masked) {
-    const Tile<D>& t = tiles[step & 1];
-    float16v sc[2];
+  // 16 bytes of this lane's key: the first operand of the i-th product of the kb-th 32 keys
+  auto key_part = [&](const uint8_t* t, int kb, int i) {
+    return *(const bf16x8*)(t + k_at[i % 4] + i / 4 * 128 + kb * 32 * kRow);
+  };
+  // that of the d-th 32 elements and the j-th 16 keys of the values
+  auto value_part = [&](const uint8_t* t, int j, int d) {
+    uint4v a;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      sc[kb] = (float16v)0.0f;
-#pragma unroll
-      for (int i = 0; i < NK; ++i) {
-        const bf16x8 a = *(const bf16x8*)(t.k + k_at[i % 4] + i / 4 * 128 + kb * 32 * kRow);
-        sc[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[i], sc[kb], 0, 0, 0);
-      }
+    for (int i = 0; i < 2; ++i) {
+      const uint8_t* at = t + v_at[d % 2] + d / 2 * 128 + (j * 16 + i * 8) * kRow;
+      const uint2v u = __builtin_bit_cast(
+          uint2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                      (__attribute__((address_space(3))) short4v*)at));
+      a[2 * i] = u[0];
+      a[2 * i + 1] = u[1];
     }
-    const int seen = limit - step * kKeys - 4 * half;  // this lane's keys below that count
-    if (masked) {
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (kb * 32 + i / 4 * 8 + i % 4 >= seen) sc[kb][i] = -INFINITY;
-    }
-    float top = sc[0][0];
-#pragma unroll
-    for (int i = 1; i < 32; ++i) top = __builtin_fmaxf(top, sc[i / 16][i % 16]);
+    return a;
+  };
+  // m and what hangs on it, for a step whose largest score of this lane's keys is top
+  auto renew = [&](float top) {
     top = __builtin_fmaxf(top, other_half(top));
     if (__any((top - m) * p.c > kSlack)) {
       const float next = __builtin_fmaxf(m, top);
@@ -274,6 +281,36 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
       for (int i = 0; i < DT; ++i) o[i] *= f;
       large = __any(__builtin_fabsf(mc) >= kLarge);
     }
+  };
+  auto masked = [&](int step) { return step * kKeys + kKeys > all_see; };
+  auto mask = [&](int step, float16v (&sc)[2]) {
+    const int seen = limit - step * kKeys - 4 * half;  // this lane's keys below that count
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i / 16 * 32 + i % 16 / 4 * 8 + i % 4 >= seen) sc[i / 16][i % 16] = -INFINITY;
+  };
+  auto largest = [&](const float16v (&sc)[2]) {
+    float top = sc[0][0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) top = __builtin_fmaxf(top, sc[i / 16][i % 16]);
+    return top;
+  };
+  // a step's scores, masked, and m for them
+  auto score = [&](int step, float16v (&sc)[2]) {
+    const uint8_t* t = tiles.k[step & 1];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      sc[kb] = (float16v)0.0f;
+#pragma unroll
+      for (int i = 0; i < NK; ++i)
+        sc[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_part(t, kb, i), q[i], sc[kb], 0, 0, 0);
+    }
+    if (masked(step)) mask(step, sc);
+    renew(largest(sc));
+  };
+  // a step's probabilities and their product with the values
+  auto add_values = [&](int step, float16v (&sc)[2]) {
+    const uint8_t* t = tiles.v[step & 1];
     if (large) {
       const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
@@ -291,25 +328,12 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       weights[i / 4][i % 4] = pack(sc[i / 8][i % 8 * 2], sc[i / 8][i % 8 * 2 + 1]);
-    auto values = [&](int j, int d) {
-      uint4v a;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint8_t* at = t.v + v_at[d % 2] + d / 2 * 128 + (j * 16 + i * 8) * kRow;
-        const uint2v u = __builtin_bit_cast(
-            uint2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (__attribute__((address_space(3))) short4v*)at));
-        a[2 * i] = u[0];
-        a[2 * i + 1] = u[1];
-      }
-      return a;
-    };
     auto product = [&](auto clean) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          uint4v a = values(j, d);
+          uint4v a = value_part(t, j, d);
           if constexpr (decltype(clean)::value) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) a[i] = finite_part(a[i]);
@@ -322,11 +346,11 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
     // A weight of zero does not take out an infinity or NaN: where a step that not every row sees
     // whole has one, it is left out here and added behind the loop.
     bool dirty = false;
-    if (masked) {
+    if (masked(step)) {
       uint32_t bad = 0;
 #pragma unroll 4
       for (int i = lane * 16; i < kKeys * kRow; i += 1024) {
-        const uint4v u = *(const uint4v*)(t.v + i);
+        const uint4v u = *(const uint4v*)(t + i);
 #pragma unroll
         for (int x = 0; x < 4; ++x) bad |= finite_part(u[x]) ^ u[x];
       }
@@ -339,15 +363,96 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
       product(std::false_type{});
     }
   };
+  // Both at once, add_values(step, sc) and score(step + 1, next), for a step that every row sees
+  // whole: the matrix units do the next step's scores, then this one's values, and beside each of
+  // their instructions stand a few of the others' -- the probabilities in the first half (the
+  // last quarter in the second), the next step's maximum in the second -- and the reads of
+  // operands two instructions ahead.
+  auto both = [&](int step, float16v (&sc)[2], float16v (&next)[2]) {
+    constexpr int kSlots = 2 * NK;  // matrix instructions of a half (4 * DT as well)
+    constexpr int kAhead = 2;
+    const uint8_t *kt = tiles.k[(step + 1) & 1], *vt = tiles.v[step & 1];
+    uint4v weights[4];
+    auto probability = [&](int i) {
+      const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i / 16][i % 16], p.c, -mc));
+      sc[i / 16][i % 16] = x;
+      l += x;
+      if (i % 2)
+        weights[i / 8][i % 8 / 2] = pack(sc[i / 16][i % 16 - 1], x);
+    };
+    auto fetch = [&](int n) {  // the operand of the n-th instruction of both halves
+      return n < kSlots ? key_part(kt, n % 2, n / 2)
+                        : __builtin_bit_cast(bf16x8, value_part(vt, (n - kSlots) / DT,
+                                                                (n - kSlots) % DT));
+    };
+    bf16x8 ring[kAhead + 1];
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) ring[n] = fetch(n);
+    next[0] = next[1] = (float16v)0.0f;
+#pragma unroll
+    for (int n = 0; n < kSlots; ++n) {
+      ring[(n + kAhead) % (kAhead + 1)] = fetch(n + kAhead);
+      next[n % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[n % (kAhead + 1)], q[n / 2],
+                                                            next[n % 2], 0, 0, 0);
+#pragma unroll
+      for (int i = n * 24 / kSlots; i < (n + 1) * 24 / kSlots; ++i) probability(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    float top = next[0][0];
+#pragma unroll
+    for (int n = 0; n < kSlots; ++n) {
+      constexpr int kAll = 2 * kSlots;
+      if (n + kSlots + kAhead < kAll)
+        ring[(n + kSlots + kAhead) % (kAhead + 1)] = fetch(n + kSlots + kAhead);
+      const int j = n / DT, d = n % DT;
+      o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[(n + kSlots) % (kAhead + 1)],
+                                                     __builtin_bit_cast(bf16x8, weights[j]), o[d],
+                                                     0, 0, 0);
+      if (n < kSlots / 2) {
+#pragma unroll
+        for (int i = 24 + n * 16 / kSlots; i < 24 + (n + 1) * 16 / kSlots; ++i) probability(i);
+      } else {
+#pragma unroll
+        for (int i = (n - kSlots / 2) * 64 / kSlots; i < (n + 1 - kSlots / 2) * 64 / kSlots; ++i)
+          top = __builtin_fmaxf(top, next[i / 16][i % 16]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    renew(top);
+  };
 
-  if (steps > 0) copy(0);
-  for (int step = 0; step < steps; ++step) {
-    // this step's keys are there, and every wavefront is done with the tile that comes next
+  // A step's values and the next one's keys are there, and every wavefront is done with the tiles
+  // that come next.
+  auto begin = [&](int step) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (step + 1 < steps) copy(step + 1);
-    if (step * kKeys >= wave_limit) continue;
-    step_of(step, step * kKeys + kKeys > all_see);
+    copy_keys(step + 2);
+    copy_values(step + 1);
+  };
+  const int own_steps = (wave_limit + kKeys - 1) / kKeys;  // this wavefront's
+  const int whole_steps = all_see / kKeys;                 // those that all of its rows see whole
+  float16v sc[2];
+  copy_keys(0);
+  copy_values(0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  copy_keys(1);
+  if (own_steps > 0) score(0, sc);
+  int step = 0;
+#pragma unroll 1
+  for (; step + 1 < whole_steps && !large; ++step) {
+    float16v next[2];
+    begin(step);
+    both(step, sc, next);
+    sc[0] = next[0];
+    sc[1] = next[1];
+  }
+#pragma unroll 1
+  for (; step < steps; ++step) {
+    begin(step);
+    if (step >= own_steps) continue;
+    add_values(step, sc);
+    if (step + 1 < own_steps) score(step + 1, sc);
   }
 
   if (any_dirty) {
