@@ -26,6 +26,9 @@
 // numbers run over key heads first, so that a key head's workgroups meet in
 // the same dies' L2, and the last rows of a sequence, which see the most keys,
 // start first.
+#include <algorithm>
+#include <cmath>
+
 #include "layer_launch.h"
 #include "rollout_divisor.h"
 
@@ -40,10 +43,14 @@ typedef float float16v __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int kKeys = 64;  // of a step
+constexpr int kWaves = 4, kRows = 32 * kWaves;  // of a workgroup
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kSlack = 8.0f;       // powers of two by which scores may pass m
 constexpr float kLarge = 0x1p20f;
+
+// The same value in every lane, said so.
+__device__ __forceinline__ int32_t same(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 
 struct Params {
   const uint16_t *q, *k, *v;
@@ -55,6 +62,9 @@ struct Params {
   Divisor kv_heads;
   Divisor per_head;  // query heads of a key head
   int32_t blocks;    // of a key head: room for all sequences' row blocks
+  Divisor parts;     // that a block's steps are cut into
+  float* part_o;     // [parts][q_tokens][q_heads][D], where there are several
+  float2* part_ml;
   uint32_t first_block;
   float c;           // |scale| log2(e)
   uint32_t sign;     // 0x80008000 for a negative scale
@@ -65,29 +75,64 @@ struct Sequence {
   int32_t q0, m, k0, n;
 };
 
-// Sequence b's row blocks are numbered from q_offsets[b] * per_head / RB + b on, which leaves room
-// for all of them: rows / RB, rounded up, is at most one more than the difference of that quotient.
-template <int RB>
-__device__ __forceinline__ int first_number(const Params& p, int b) {
-  const int32_t q0 = min(max(p.q_offsets[b], 0), p.q_tokens);
-  return (int)((uint32_t)q0 * p.per_head.d / RB) + b;
+__device__ __forceinline__ Sequence sequence(const Params& p, int b) {
+  Sequence s;
+  s.q0 = min(max(p.q_offsets[b], 0), p.q_tokens);
+  s.m = min(max(p.q_offsets[b + 1], s.q0), p.q_tokens) - s.q0;
+  s.k0 = min(max(p.k_offsets[b], 0), p.k_tokens);
+  s.n = min(max(p.k_offsets[b + 1], s.k0), p.k_tokens) - s.k0;
+  return s;
 }
 
-// The last sequence whose first number is at most w; 64 candidates at a time.
-template <int RB>
-__device__ __forceinline__ int sequence_of(const Params& p, int w) {
+// A block of rows of a sequence (block < 0 or past the last: none).
+struct Block {
+  Sequence s;
+  int block;
+};
+
+// Blocks in the sequences' order: sequence b's are numbered from q_offsets[b] * per_head /
+// kRows + b on, which leaves room for all of them: rows / kRows, rounded up, is at most one more than the
+// difference of that quotient.
+__device__ __forceinline__ Block block_by_place(const Params& p, int w) {
   const int lane = threadIdx.x % 64;
-  int lo = 0, count = p.batch;  // it is one of [lo, lo + count); lo's number is at most w, or lo is 0
+  auto first_of = [&](int b) {
+    const int32_t q0 = min(max(p.q_offsets[b], 0), p.q_tokens);
+    return (int)((uint32_t)q0 * p.per_head.d / kRows) + b;
+  };
+  // the last sequence whose first number is at most w, 64 candidates at a time: one of
+  // [lo, lo + count), lo's number is at most w, or lo is 0
+  int lo = 0, count = p.batch;
   while (count > 1) {
     const int step = (count + 63) / 64;
     const int at = lo + lane * step;
-    const bool below = at < lo + count && first_number<RB>(p, at) <= w;
+    const bool below = at < lo + count && first_of(at) <= w;
     const uint64_t set = __ballot(below);
     const int last = set == 0 ? 0 : 63 - __builtin_clzll(set);
     count = min(step, lo + count - (lo + last * step));
     lo += last * step;
   }
-  return __builtin_amdgcn_readfirstlane(lo);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  return Block{sequence(p, lo), w - first_of(lo)};
+}
+
+// Blocks in falling order of their sequences' keys, and from the last to the first of a sequence:
+// a lane a sequence, up to 64 of them.  What starts last is short; and a sequence's blocks are
+// neighbours, so that its keys are met in L2.
+__device__ __forceinline__ Block block_by_length(const Params& p, int w) {
+  const int lane = threadIdx.x % 64;
+  Sequence s{0, 0, 0, 0};
+  if (lane < p.batch) s = sequence(p, lane);
+  const int blocks = (int)(((uint32_t)s.m * p.per_head.d + kRows - 1) / kRows);
+  int before = 0;
+  for (int i = 0; i < p.batch; ++i) {
+    const int n = __builtin_amdgcn_readlane(s.n, i), c = __builtin_amdgcn_readlane(blocks, i);
+    before += n > s.n || (n == s.n && i < lane) ? c : 0;
+  }
+  const uint64_t is = __ballot(lane < p.batch && w >= before && w < before + blocks);
+  if (is == 0) return Block{{0, 0, 0, 0}, -1};
+  const int b = __builtin_ctzll(is);
+  auto of = [&](int v) { return __builtin_amdgcn_readlane(v, b); };
+  return Block{{of(s.q0), of(s.m), of(s.k0), of(s.n)}, of(before + blocks) - 1 - w};
 }
 
 // 16 bytes a lane, from base + scalar + lane's offset to lds + 16 * lane.  (Written out: the
@@ -96,7 +141,7 @@ __device__ __forceinline__ int sequence_of(const Params& p, int w) {
 // m0 holds nothing of the compiler's here.)
 __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t base, uint32_t lane, uint32_t scalar,
                                        uint8_t* lds) {
-  const uint32_t at = (uint32_t)(uintptr_t)(lds_void*)lds;
+  const uint32_t at = (uint32_t)same((int32_t)(uint32_t)(uintptr_t)(lds_void*)lds);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(at), "v"(lane), "s"(base), "s"(scalar)
@@ -115,8 +160,10 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// The order of a row's 16-byte pieces, exchanged within 8 of them: for eight neighbouring keys
-// all different, for four also without the lowest bit.
+// The places of a row's 16-byte pieces are exchanged so that no two lanes of a read meet in a
+// bank.  LDS has 64 banks of 4 bytes: 16 lanes read 16 bytes each, of 16 neighbouring keys at the
+// same place, at once; these have to lie differently in 256 bytes.  A transposing read takes 8
+// bytes of 16 lanes, 32 bytes of four neighbouring keys.
 __device__ __forceinline__ int turned(int key) { return (key & 3) << 1 | (key >> 2 & 1); }
 
 // Two BF16 numbers with zeros for infinities and NaN.
@@ -126,31 +173,33 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t w) {
 }
 
 template <int D>
-struct Tiles {
+struct Tiles {  // one step's in use, the next one's in flight
   alignas(16) uint8_t k[2][kKeys * D * 2];
   alignas(16) uint8_t v[2][kKeys * D * 2];
 };
 
-template <int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(const Params p) {
-  constexpr int RB = 32 * WAVES, NK = D / 16, DT = D / 32, kRow = 2 * D;
+template <int D>
+__global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(const Params p) {
+  // whether the next step's scores may be masked where they are computed beside the values'
+  // product (heads of 256 have no registers for it: 583 us instead of 331 for 4096 tokens)
+  constexpr bool kMaskNext = D < 256;
+  constexpr int NK = D / 16, DT = D / 32, kRow = 2 * D;
   __shared__ Tiles<D> tiles;
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int col = lane % 32, half = lane / 32;
 
+  // numbers: key heads first, then parts, then blocks
   const uint32_t id = p.first_block + blockIdx.x;
-  const uint32_t w_up = quotient(id, p.kv_heads);
-  const int kvh = (int)(id - w_up * p.kv_heads.d);
-  const int w = p.blocks - 1 - (int)w_up;
-  const int b = sequence_of<RB>(p, w);
-  Sequence s;
-  s.q0 = min(max(p.q_offsets[b], 0), p.q_tokens);
-  s.m = min(max(p.q_offsets[b + 1], s.q0), p.q_tokens) - s.q0;
-  s.k0 = min(max(p.k_offsets[b], 0), p.k_tokens);
-  s.n = min(max(p.k_offsets[b + 1], s.k0), p.k_tokens) - s.k0;
+  uint32_t w = quotient(id, p.kv_heads);
+  const int kvh = (int)(id - w * p.kv_heads.d);
+  const uint32_t nth = quotient(w, p.parts);
+  const int part = (int)(w - nth * p.parts.d);
+  const Block at = p.batch <= 64 ? block_by_length(p, (int)nth)
+                                 : block_by_place(p, p.blocks - 1 - (int)nth);
+  const Sequence s{same(at.s.q0), same(at.s.m), same(at.s.k0), same(at.s.n)};
   const int rows = (int)((uint32_t)s.m * p.per_head.d);
-  const int64_t row0 = ((int64_t)w - first_number<RB>(p, b)) * RB;
-  if (row0 < 0 || row0 >= rows) return;
+  const int64_t row0 = (int64_t)same(at.block) * kRows;
+  if (at.block < 0 || row0 >= rows) return;
 
   // rows past the last are the last once more, and not stored
   auto limit_of = [&](int r) {  // keys that row r sees
@@ -160,32 +209,22 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
   const int token = (int)quotient((uint32_t)r, p.per_head);
   const int head = kvh * (int)p.per_head.d + r - token * (int)p.per_head.d;
   const int limit = limit_of(r);
-  const int block_limit = limit_of((int)row0 + RB - 1);
+  const int block_limit = limit_of((int)row0 + kRows - 1);
   const int wave_limit = first < rows ? limit_of(first + 31) : 0;  // the most any row sees,
   const int all_see = limit_of(first);                             // and the least
-  const int steps = (block_limit + kKeys - 1) / kKeys;
+  // the part's steps
+  const int all_steps = (block_limit + kKeys - 1) / kKeys;
+  const int share = (int)quotient((uint32_t)all_steps + p.parts.d - 1, p.parts);
+  const int begin_step = part * share, steps = min(begin_step + share, all_steps);
 
-  // queries, as the scores' second operand
-  bf16x8 q[NK];
-  {
-    const uint16_t* from = p.q + (int64_t)(s.q0 + token) * p.q_stride + head * D + half * 8;
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      uint4v u = *(const uint4v*)(from + i * 16);
-      u ^= p.sign;
-      q[i] = __builtin_bit_cast(bf16x8, u);
-    }
-  }
-
-  // A step's copies: this wavefront's keys are the (64 / WAVES) from wave * 64 / WAVES on; the
-  // order of the pieces comes again every 8 keys, which are kPeriod copies.
-  constexpr int kPeriod = D / 64, kEights = 8 / WAVES;
+  // A step's copies: this wavefront's keys are the 16 from wave * 16 on, D / 64 copies for every eight; the pieces' order comes again with these.
+  constexpr int kPeriod = D / 64, kLoads = kKeys / kWaves / 8 * kPeriod;
   const char* k_base = (const char*)(p.k + (int64_t)s.k0 * p.k_stride + kvh * D);
   const char* v_base = (const char*)(p.v + (int64_t)s.k0 * p.v_stride + kvh * D);
   const uint32_t k_row = (uint32_t)p.k_stride * 2, v_row = (uint32_t)p.v_stride * 2;  // bytes
-  auto piece_of = [&](int n, int& key, uint32_t& in_row) {  // of the n-th copy of eight keys
+  auto piece_of = [&](int n, int& key, uint32_t& in_row) {  // this lane's of the n-th copy
     const int piece = n * 64 + lane;
-    key = piece / (D / 8);
+    key = wave * (kKeys / kWaves) + piece / (D / 8);
     in_row = (uint32_t)(piece % (D / 8) ^ turned(key)) * 16;
   };
   uint32_t k_from[kPeriod], v_from[kPeriod];
@@ -197,40 +236,54 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
     k_from[n] = key * k_row + in_row;
     v_from[n] = key * v_row + in_row;
   }
+  auto source = [&](const char* base, uint32_t row, int step) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(base + (int64_t)step * kKeys * row), 0, -1,
+                                             0x20000);
+  };
+  auto copy_one = [&](int n, int step, __amdgpu_buffer_rsrc_t at, uint32_t row,
+                      const uint32_t (&from)[kPeriod], uint8_t (&tile)[2][kKeys * D * 2]) {
+    to_lds(at, from[n % kPeriod], n / kPeriod * 8 * row,
+           tile[step & 1] + (wave * kLoads + n) * 1024);
+  };
   // a step's keys (or values) to tile step % 2
   auto copy = [&](int step, const char* base, uint32_t row, const uint32_t (&from)[kPeriod],
                   uint8_t (&tile)[2][kKeys * D * 2]) {
-    uint8_t* t = tile[step & 1] + wave * kEights * kPeriod * 1024;
-    const auto at = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(base + (int64_t)step * kKeys * row), 0, -1, 0x20000);
-    const uint32_t key0 = wave * kEights * 8;
+    if (step >= steps) return;
+    const auto at = source(base, row, step);
     if (step * kKeys + kKeys <= s.n) {
 #pragma unroll
-      for (int e = 0; e < kEights; ++e)
-#pragma unroll
-        for (int n = 0; n < kPeriod; ++n)
-          to_lds(at, from[n], (key0 + e * 8) * row, t + (e * kPeriod + n) * 1024);
+      for (int n = 0; n < kLoads; ++n) copy_one(n, step, at, row, from, tile);
     } else {
       // keys past the sequence's end are its last once more
 #pragma unroll 1
-      for (int e = 0; e < kEights; ++e) {
-#pragma unroll 1
-        for (int n = 0; n < kPeriod; ++n) {
-          int key;
-          uint32_t in_row;
-          piece_of(n, key, in_row);
-          const uint32_t k = min((int)key0 + e * 8 + key, s.n - 1 - step * kKeys);
-          to_lds(at, k * row + in_row, 0, t + (e * kPeriod + n) * 1024);
-        }
+      for (int n = 0; n < kLoads; ++n) {
+        int key;
+        uint32_t in_row;
+        piece_of(n, key, in_row);
+        to_lds(at, (uint32_t)min(key, s.n - 1 - step * kKeys) * row + in_row, 0,
+               tile[step & 1] + (wave * kLoads + n) * 1024);
       }
     }
   };
-  auto copy_keys = [&](int step) {
-    if (step < steps) copy(step, k_base, k_row, k_from, tiles.k);
+  // Copies go in pairs, a step's values and the next one's keys, one step ahead.
+  auto copy_pair = [&](int step) {
+    copy(step, v_base, v_row, v_from, tiles.v);
+    copy(step + 1, k_base, k_row, k_from, tiles.k);
   };
-  auto copy_values = [&](int step) {
-    if (step < steps) copy(step, v_base, v_row, v_from, tiles.v);
-  };
+
+  int step = begin_step;
+  copy(step, k_base, k_row, k_from, tiles.k);
+  // queries, as the scores' second operand
+  bf16x8 q[NK];
+  {
+    const uint16_t* from = p.q + (int64_t)(s.q0 + token) * p.q_stride + head * D + half * 8;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      uint4v u = *(const uint4v*)(from + i * 16);
+      u ^= p.sign;
+      q[i] = __builtin_bit_cast(bf16x8, u);
+    }
+  }
 
   float16v o[DT];
 #pragma unroll
@@ -368,7 +421,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
   // their instructions stand a few of the others' -- the probabilities in the first half (the
   // last quarter in the second), the next step's maximum in the second -- and the reads of
   // operands two instructions ahead.
-  auto both = [&](int step, float16v (&sc)[2], float16v (&next)[2]) {
+  auto both = [&](int step, float16v (&sc)[2], float16v (&next)[2], auto copies) {
     constexpr int kSlots = 2 * NK;  // matrix instructions of a half (4 * DT as well)
     constexpr int kAhead = 2;
     const uint8_t *kt = tiles.k[(step + 1) & 1], *vt = tiles.v[step & 1];
@@ -394,6 +447,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
       ring[(n + kAhead) % (kAhead + 1)] = fetch(n + kAhead);
       next[n % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[n % (kAhead + 1)], q[n / 2],
                                                             next[n % 2], 0, 0, 0);
+      copies(n);
 #pragma unroll
       for (int i = n * 24 / kSlots; i < (n + 1) * 24 / kSlots; ++i) probability(i);
       __builtin_amdgcn_sched_barrier(0);
@@ -418,38 +472,57 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (kMaskNext) {
+      if (masked(step + 1)) {
+        mask(step + 1, next);
+        top = largest(next);
+      }
+    }
     renew(top);
   };
 
-  // A step's values and the next one's keys are there, and every wavefront is done with the tiles
-  // that come next.
-  auto begin = [&](int step) {
+  // A step's pair is there, and every wavefront is done with the tiles that come next.
+  auto begin = [&]() {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    copy_keys(step + 2);
-    copy_values(step + 1);
   };
-  const int own_steps = (wave_limit + kKeys - 1) / kKeys;  // this wavefront's
-  const int whole_steps = all_see / kKeys;                 // those that all of its rows see whole
+  const int own_steps = min((wave_limit + kKeys - 1) / kKeys, steps);  // this wavefront's end
+  const int whole_steps = min(all_see / kKeys, steps);  // end of those that all its rows see whole
   float16v sc[2];
-  copy_keys(0);
-  copy_values(0);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  copy_keys(1);
-  if (own_steps > 0) score(0, sc);
-  int step = 0;
+  begin();
+  copy_pair(step);
+  if (step < own_steps) score(step, sc);
+  // (while the pair that is copied meanwhile exists to its last key)
+  const int full_steps = min(whole_steps - 1, min(steps, s.n / kKeys) - 2);
 #pragma unroll 1
-  for (; step + 1 < whole_steps && !large; ++step) {
+  for (; step < full_steps && !large; ++step) {
     float16v next[2];
-    begin(step);
-    both(step, sc, next);
+    begin();
+    const auto values = source(v_base, v_row, step + 1);
+    const auto keys = source(k_base, k_row, step + 2);
+    both(step, sc, next, [&](int n) {
+      if (n < kLoads)
+        copy_one(n, step + 1, values, v_row, v_from, tiles.v);
+      else if (n < 2 * kLoads)
+        copy_one(n - kLoads, step + 2, keys, k_row, k_from, tiles.k);
+    });
+    sc[0] = next[0];
+    sc[1] = next[1];
+  }
+  const int last_whole = kMaskNext ? min(whole_steps, own_steps - 1) : whole_steps - 1;
+#pragma unroll 1
+  for (; step < last_whole && !large; ++step) {
+    float16v next[2];
+    begin();
+    copy_pair(step + 1);
+    both(step, sc, next, [](int) {});
     sc[0] = next[0];
     sc[1] = next[1];
   }
 #pragma unroll 1
   for (; step < steps; ++step) {
-    begin(step);
+    begin();
+    copy_pair(step + 1);
     if (step >= own_steps) continue;
     add_values(step, sc);
     if (step + 1 < own_steps) score(step + 1, sc);
@@ -457,9 +530,11 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
 
   if (any_dirty) {
     // values that are not finite, of the steps that were masked, to the rows that see them
-    const char* from = v_base + (int64_t)(all_see / kKeys * kKeys) * v_row + 8 * half;
+    const int from_key = max(all_see / kKeys, begin_step) * kKeys;
+    const int to_key = min(wave_limit, steps * kKeys);
+    const char* from = v_base + (int64_t)from_key * v_row + 8 * half;
 #pragma unroll 1
-    for (int key = all_see / kKeys * kKeys; key < wave_limit; ++key, from += v_row) {
+    for (int key = from_key; key < to_key; ++key, from += v_row) {
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -476,26 +551,101 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void prompt_kernel(co
   }
 
   l += other_half(l);
-  const float each = l == 0.0f ? 0.0f : 1.0f / l;
-  if (first + col < rows) {
-    const int64_t row = (int64_t)(s.q0 + token) * p.q_heads + head;
-    uint16_t* to = p.out + row * D + 4 * half;
+  if (first + col >= rows) return;
+  const int64_t row = (int64_t)(s.q0 + token) * p.q_heads + head;
+  if (p.parts.d > 1) {
+    const int64_t at_part = part * (int64_t)p.q_tokens * p.q_heads + row;
+    if (half == 0) p.part_ml[at_part] = make_float2(m, l);
+    if (l == 0.0f) return;
+    float* to = p.part_o + at_part * D + 4 * half;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint2v u = {pack(o[d][4 * i] * each, o[d][4 * i + 1] * each),
-                          pack(o[d][4 * i + 2] * each, o[d][4 * i + 3] * each)};
-        *(uint2v*)(to + d * 32 + i * 8) = u;
-      }
-    if (p.lse && half == 0)
-      p.lse[row] = l == 0.0f ? -INFINITY : (mc + __builtin_amdgcn_logf(l)) * kLn2;
+      for (int i = 0; i < 4; ++i)
+        *(float4*)(to + d * 32 + i * 8) =
+            make_float4(o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]);
+    return;
   }
+  const float each = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* to = p.out + row * D + 4 * half;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint2v u = {pack(o[d][4 * i] * each, o[d][4 * i + 1] * each),
+                        pack(o[d][4 * i + 2] * each, o[d][4 * i + 3] * each)};
+      *(uint2v*)(to + d * 32 + i * 8) = u;
+    }
+  if (p.lse && half == 0)
+    p.lse[row] = l == 0.0f ? -INFINITY : (mc + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// The parts of a row to its output, in order.  A wavefront takes a row, a lane D / 64 elements.
+template <int D>
+__global__ __launch_bounds__(256) void prompt_join(const Params p) {
+  constexpr int E = D / 64;
+  const int lane = threadIdx.x % 64;
+  const int64_t all = (int64_t)p.q_tokens * p.q_heads;
+  const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  if (row >= all) return;
+  // rows of no sequence are left as they are
+  const int64_t lo = min(max(p.q_offsets[0], 0), p.q_tokens);
+  const int64_t hi = min(max(p.q_offsets[p.batch], 0), p.q_tokens);
+  if (row < lo * p.q_heads || row >= hi * p.q_heads) return;
+  const int parts = (int)p.parts.d;
+  float top = -INFINITY;
+  for (int i = 0; i < parts; ++i) {
+    const float2 ml = p.part_ml[i * all + row];
+    if (ml.y != 0.0f) top = __builtin_fmaxf(top, ml.x);
+  }
+  float l = 0.0f, o[E] = {};
+  for (int i = 0; i < parts; ++i) {
+    const float2 ml = p.part_ml[i * all + row];
+    if (ml.y == 0.0f) continue;  // (nothing was written)
+    const float f = __builtin_amdgcn_exp2f((ml.x - top) * p.c);
+    l = __builtin_fmaf(ml.y, f, l);
+    const float* from = p.part_o + (i * all + row) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(from[e], f, o[e]);
+  }
+  const float each = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    p.out[row * D + lane * E + e] = (uint16_t)(pack(o[e] * each, 0.0f) & 0xffffu);
+  if (p.lse && lane == 0)
+    p.lse[row] = l == 0.0f ? -INFINITY : (top * p.c + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 }  // namespace
 
-int64_t prompt_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+namespace {
+
+// Parts that the steps of every block are cut into.  A step takes about D / 128 us, however few
+// blocks there are; a part costs its rows' sums, written and read in FP32 (3 TB/s), and 0.5 us, and
+// the join 4 us.  So the steps are cut in the square root of their time by a part's, up to two
+// workgroups a compute unit, where there are 12 us of them.  Measured, with 32 heads on 8 of 128
+// but for the last, whole and in 2, 4, 8 and 16 parts (the rule's number first):
+//   16 queries behind 8000 keys  (13) 130, 74, 43, 30, 27 us     64 behind 2000  (5) 42, 30, 22, 21, 26
+//   256 behind 4000               (4)  75, 48, 36, 41, 58       8 times 16 behind 1000  (2) 25, 22, 21, 25, 36
+//   512 behind 16000              (3) 260, 163, 156, 170, 209   512 behind 512  (1) 26, 26, 31, 48, 78
+//   512, 8 heads on 2 of 256, behind 4000  (7) 136, 81, 54, 44, 63
+int64_t parts_of(int64_t q_tokens, int64_t q_heads, int64_t k_tokens, int64_t kv_heads,
+                 int64_t head_dim, int64_t batch) {
+  const int64_t groups = (q_tokens * (q_heads / kv_heads) / kRows + batch) * kv_heads;
+  const double steps = (double)k_tokens / batch / kKeys * head_dim / 128;  // us
+  const double part = 0.5 + (double)q_tokens * q_heads * head_dim * 8 / 3e6;
+  if (steps < 12) return 1;
+  const int64_t parts = std::min((int64_t)std::sqrt(steps / part), 512 / groups);
+  return std::min(std::max(parts, (int64_t)1), (int64_t)64);
+}
+
+}  // namespace
+
+int64_t prompt_workspace_bytes(int64_t q_tokens, int64_t q_heads, int64_t k_tokens,
+                               int64_t kv_heads, int64_t head_dim, int64_t batch) {
+  const int64_t parts = parts_of(q_tokens, q_heads, k_tokens, kv_heads, head_dim, batch);
+  return parts == 1 ? 0 : parts * q_tokens * q_heads * (head_dim + 2) * 4;
+}
 
 hipError_t prompt_launch(const PromptArgs& a, hipStream_t stream) {
   Params p{};
@@ -518,22 +668,34 @@ hipError_t prompt_launch(const PromptArgs& a, hipStream_t stream) {
   const float c = __builtin_fabsf(a.scale) * kLog2e;
   p.c = c > 0x1p-126f ? c : 0x1p-126f;  // (zero times an infinite score would be NaN)
   p.sign = a.scale < 0.0f ? 0x80008000u : 0u;
-  constexpr int kWaves = 4;
-  p.blocks = (int32_t)(a.q_tokens * p.per_head.d / (32 * kWaves) + a.batch);
-  const int64_t total = (int64_t)p.blocks * a.kv_heads;
-  const int64_t most = ((int64_t)1 << 32) / (64 * kWaves) - 1;
-  for (int64_t first = 0; first < total; first += most) {
-    p.first_block = (uint32_t)first;
-    const uint32_t grid = (uint32_t)(total - first < most ? total - first : most);
-    const void* kernel = a.head_dim == 64    ? (void*)prompt_kernel<64, kWaves>
-                         : a.head_dim == 128 ? (void*)prompt_kernel<128, kWaves>
-                         : a.head_dim == 192 ? (void*)prompt_kernel<192, kWaves>
-                                             : (void*)prompt_kernel<256, kWaves>;
+  const int64_t parts = parts_of(a.q_tokens, a.q_heads, a.k_tokens, a.kv_heads,
+                                 a.head_dim, a.batch);
+  p.parts = divisor_of((uint32_t)parts);
+  p.part_o = (float*)a.workspace;
+  if (parts > 1)
+    p.part_ml = (float2*)(p.part_o + parts * a.q_tokens * a.q_heads * a.head_dim);
+  p.blocks = (int32_t)(a.q_tokens * p.per_head.d / kRows + a.batch);
+  auto launch = [&](const void* kernel, const void* join) {
+    const int64_t total = (int64_t)p.blocks * a.kv_heads * parts;
+    const int64_t most = ((int64_t)1 << 32) / (64 * kWaves) - 1;  // (a launch holds 2^32 threads)
     void* args[] = {&p};
-    const hipError_t e = hipLaunchKernel(kernel, dim3(grid), dim3(64 * kWaves), args, 0, stream);
-    if (e != hipSuccess) return e;
+    hipError_t e = hipSuccess;
+    for (int64_t first = 0; first < total && e == hipSuccess; first += most) {
+      p.first_block = (uint32_t)first;
+      const uint32_t grid = (uint32_t)(total - first < most ? total - first : most);
+      e = hipLaunchKernel(kernel, dim3(grid), dim3(64 * kWaves), args, 0, stream);
+    }
+    if (parts > 1 && e == hipSuccess)
+      e = hipLaunchKernel(join, dim3((uint32_t)((a.q_tokens * a.q_heads + 3) / 4)), dim3(256), args,
+                          0, stream);
+    return e;
+  };
+  switch (a.head_dim) {
+    case 64: return launch((void*)prompt_kernel<64>, (void*)prompt_join<64>);
+    case 128: return launch((void*)prompt_kernel<128>, (void*)prompt_join<128>);
+    case 192: return launch((void*)prompt_kernel<192>, (void*)prompt_join<192>);
+    default: return launch((void*)prompt_kernel<256>, (void*)prompt_join<256>);
   }
-  return hipSuccess;
 }
 
 }  // namespace fp4q

@@ -259,6 +259,60 @@ def test_scores_of_minus_infinity():
     assert torch.allclose(out[2:, 0].double(), want, atol=0.03, rtol=0.02)
 
 
+# contexts that are cut into parts, where queries are few (several launches)
+PARTS = [(64, 8, 2, [3], [2500]), (128, 8, 1, [1], [5000]), (128, 8, 2, [40, 1, 0, 7], [3000, 2000, 1500, 5]),
+         (192, 4, 4, [20], [3100]), (256, 4, 2, [5, 30], [1200, 3000]), (128, 2, 1, [64], [64 * 40]),
+         (64, 6, 3, [9, 4], [0, 9000]), (256, 2, 2, [33], [1601])]
+
+
+@pytest.mark.parametrize("d,h,hk,q_lens,k_lens", PARTS)
+def test_few_queries_behind_long_contexts(d, h, hk, q_lens, k_lens):
+    q, k, v = inputs(q_lens, k_lens, h, hk, d, seed=41, gain=1.5)
+    assert fq.rollout_lib().prompt_attention_workspace_bytes(len(q), h, len(k), hk, d, len(q_lens)) > 0
+    out, lse = fq.prompt_attention(q, k, v, offsets(q_lens), offsets(k_lens), lse=True)
+    check(q, k, v, q_lens, k_lens, out, lse, label="parts")
+    assert torch.equal(fq.prompt_attention(q, k, v, offsets(q_lens), offsets(k_lens)), out)
+    # as one call of many sequences, which are not cut, gives it
+    both = (torch.cat([q] * 70), torch.cat([k] * 70), torch.cat([v] * 70))
+    off = offsets(q_lens * 70), offsets(k_lens * 70)
+    whole = fq.prompt_attention(*both, *off)
+    check(q, k, v, q_lens, k_lens, whole[:len(q)], label="whole")
+    assert torch.equal(whole[:len(q)], whole[-len(q):])
+
+
+def test_parts_with_values_that_are_not_finite():
+    q_lens, k_lens = [12, 3], [2000, 1800]
+    q, k, v = inputs(q_lens, k_lens, 4, 2, 128, seed=43)
+    args = offsets(q_lens), offsets(k_lens)
+    clean = fq.prompt_attention(q, k, v, *args)
+    vv = v.clone()
+    vv[100, 0, 3] = math.inf            # seen by every query of the first sequence
+    vv[1995, 1, 9] = -math.inf          # by its last five (12 of 2000: from 1988 on)
+    vv[2000 + 1799, 0, 1] = math.nan    # by the last query of the second
+    vv[2000, 1, 127] = math.nan
+    out = fq.prompt_attention(q, k, vv, *args).float()
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[:12, :2, 3] = bad[7:12, 2:, 9] = bad[14, :2, 1] = bad[12:, 2:, 127] = True
+    assert not torch.isfinite(out[bad]).any()
+    assert torch.equal(out[~bad], clean.float()[~bad])
+    # rows of no sequence stay, also behind a join
+    big = torch.full((len(q) + 9, 4, 128), 3.0, device="cuda").bfloat16()
+    qq = torch.cat([q[:4], q, q[:5]])
+    fq.prompt_attention(qq, k, v, args[0] + 4, args[1], out=big)
+    assert torch.equal(big[4:4 + len(q)], clean) and (big[:4] == 3).all() and (big[4 + len(q):] == 3).all()
+
+
+def test_workspaces():
+    q, k, v = inputs([4], [4000], 4, 2, 128, seed=45)
+    args = (q, k, v, offsets([4]), offsets([4000]))
+    need = fq.rollout_lib().prompt_attention_workspace_bytes(4, 4, 4000, 2, 128, 1)
+    out = fq.prompt_attention(*args)
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")  # contents are ignored
+    assert torch.equal(fq.prompt_attention(*args, workspace=ws), out)
+    with pytest.raises(fq.Fp4qError):
+        fq.prompt_attention(*args, workspace=ws[:need - 1])
+
+
 def test_keys_past_32_bit_offsets():
     # rows of keys and values far apart: the last begins beyond 2^31 elements
     n, stride = 300, 1 << 23
