@@ -22,6 +22,9 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kChunk = 2048;       // choices of a workgroup that counts or places
 constexpr int64_t kFew = 4096;     // choices up to which one launch does everything
 constexpr int kMaxExperts = 1024, kMaxChoices = 64;
+constexpr int64_t kLastLevel = 256 << 20;  // bytes of the cache in front of memory
+
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
 
 struct Params {
   const char* x;
@@ -66,16 +69,29 @@ __device__ __forceinline__ int scan_counts(int* counts, int experts, int (&share
   return all;
 }
 
-// V bytes at a time from a token's row to the places of its choices.
-template <class V>
-__device__ __forceinline__ void copy_row(const Params& p, int64_t token, const int* place, int first,
-                                         int step) {
+// One V at a time from a token's row to the places of its choices, RUN of them, `step` apart, to
+// one place before the next.  ONCE: past the caches.
+template <class V, int RUN, bool ONCE>
+__device__ __forceinline__ void copy_row(const Params& p, int64_t token, const int* place,
+                                         int64_t first, int step) {
   const int64_t bytes = p.hidden * 2, pieces = bytes / (int64_t)sizeof(V);
   const V* from = (const V*)(p.x + token * bytes);
-  for (int64_t i = first; i < pieces; i += step) {
-    const V v = from[i];
-    for (int j = 0; j < (int)p.top_k.d; ++j)
-      if (place[j] >= 0) ((V*)(p.rows + (int64_t)place[j] * bytes))[i] = v;
+  for (int64_t i = first; i < pieces; i += RUN * step) {
+    V v[RUN];
+#pragma unroll
+    for (int r = 0; r < RUN; ++r) v[r] = from[min(i + r * step, pieces - 1)];
+    for (int j = 0; j < (int)p.top_k.d; ++j) {
+      if (place[j] < 0) continue;
+      V* to = (V*)(p.rows + (int64_t)place[j] * bytes);
+#pragma unroll
+      for (int r = 0; r < RUN; ++r) {
+        if (i + r * step >= pieces) break;
+        if constexpr (ONCE)
+          __builtin_nontemporal_store(v[r], to + i + r * step);
+        else
+          to[i + r * step] = v[r];
+      }
+    }
   }
 }
 
@@ -111,7 +127,8 @@ __global__ __launch_bounds__(kThreads) void dispatch_few(const Params p) {
     if (blockIdx.y == 0) p.place[own + tid] = at;
   }
   __syncthreads();
-  copy_row<V>(p, blockIdx.x, places, blockIdx.y * kThreads + tid, gridDim.y * kThreads);
+  copy_row<V, 1, false>(p, blockIdx.x, places, blockIdx.y * kThreads + tid,
+                        gridDim.y * kThreads);
 }
 
 __global__ __launch_bounds__(kThreads) void count_chunks(const Params p) {
@@ -208,12 +225,12 @@ __global__ __launch_bounds__(kThreads) void place_chunks(const Params p) {
 }
 
 // A wavefront a token at a time.
-template <class V>
+template <class V, bool ONCE>
 __global__ __launch_bounds__(kThreads) void copy_rows(const Params p) {
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < p.tokens;
        t += (int64_t)gridDim.x * kWaves)
-    copy_row<V>(p, t, p.place + t * p.top_k.d, lane, 64);
+    copy_row<V, 4, ONCE>(p, t, p.place + t * p.top_k.d, lane, 64);
 }
 
 struct Sums {
@@ -260,9 +277,12 @@ __device__ __forceinline__ void store_run(char* base, int64_t at, const float (&
   }
 }
 
-// A workgroup takes a token and a part of its columns; a thread N of them.
+// A workgroup takes a token and a part of its columns; a thread N of them.  The rows of eight
+// choices are asked for at once (with a branch at
+// each, one at a time): a choice without a row reads row 0, and takes nothing of it.
 template <class T, class O, int N>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const Sums p) {
+  constexpr int kBatch = 8;
   for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
     const int32_t* place = p.place + t * p.top_k;
     const float* weights = p.weights + t * p.top_k;
@@ -272,15 +292,21 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const Sums p) {
 #pragma unroll
       for (int i = 0; i < N; ++i) sum[i] = 0.0f;
       if (p.add) load_run<__bf16, N>(p.add, t * p.n + c, sum);
-#pragma unroll 4
-      for (int j = 0; j < p.top_k; ++j) {
-        const int at = place[j];
-        if (at < 0 || at >= p.y_rows) continue;
-        const float w = weights[j];
-        float v[N];
-        load_run<T, N>(p.y, at * p.n + c, v);
+      for (int j0 = 0; j0 < p.top_k && p.y_rows > 0; j0 += kBatch) {
+        float v[kBatch][N], w[kBatch];
+        bool has[kBatch];
 #pragma unroll
-        for (int i = 0; i < N; ++i) sum[i] = __builtin_fmaf(w, v[i], sum[i]);
+        for (int j = 0; j < kBatch; ++j) {
+          const int choice = min(j0 + j, p.top_k - 1), at = place[choice];
+          has[j] = j0 + j < p.top_k && at >= 0 && at < p.y_rows;
+          w[j] = weights[choice];
+          load_run<T, N>(p.y, (has[j] ? at : 0) * p.n + c, v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            sum[i] = has[j] ? __builtin_fmaf(w[j], v[j][i], sum[i]) : sum[i];
       }
       store_run<O, N>(p.out, t * p.n + c, sum);
     }
@@ -316,7 +342,7 @@ hipError_t dispatch_launch(const DispatchArgs& a, hipStream_t stream) {
     const int64_t most = (pieces + kThreads - 1) / kThreads;
     const dim3 grid((uint32_t)(a.tokens > 0 ? a.tokens : 1), (uint32_t)(want < most ? want : most));
     if (wide)
-      dispatch_few<uint4><<<grid, kThreads, 0, stream>>>(p);
+      dispatch_few<uint4v><<<grid, kThreads, 0, stream>>>(p);
     else
       dispatch_few<uint16_t><<<grid, kThreads, 0, stream>>>(p);
     return hipGetLastError();
@@ -325,10 +351,18 @@ hipError_t dispatch_launch(const DispatchArgs& a, hipStream_t stream) {
   place_chunks<<<p.chunks, kThreads, 0, stream>>>(p);
   const int64_t blocks = (a.tokens + kWaves - 1) / kWaves;
   const uint32_t grid = (uint32_t)(blocks < (1 << 20) ? blocks : (1 << 20));
-  if (wide)
-    copy_rows<uint4><<<grid, kThreads, 0, stream>>>(p);
+  // Rows that the last-level cache does not hold go past it: what reads them next finds most of them
+  // evicted either way, and lines that are still to be written slow it down.  Dispatch and a pass
+  // that reads its rows, past the caches and through them: 67 MB 42 and 37 us, 134 MB 74 and 71,
+  // 268 MB 141 and 143, 1.9 GB 913 and 929; and a pass that reads other memory: 39 and 48, 74 and 81,
+  // 141 and 158, 915 and 929.
+  const bool once = (int64_t)p.entries * a.hidden * 2 >= kLastLevel;
+  if (wide && once)
+    copy_rows<uint4v, true><<<grid, kThreads, 0, stream>>>(p);
+  else if (wide)
+    copy_rows<uint4v, false><<<grid, kThreads, 0, stream>>>(p);
   else
-    copy_rows<uint16_t><<<grid, kThreads, 0, stream>>>(p);
+    copy_rows<uint16_t, false><<<grid, kThreads, 0, stream>>>(p);
   return hipGetLastError();
 }
 
