@@ -11,13 +11,14 @@ __device__ __forceinline__ uint32_t moved(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
 }
 
+// Data-parallel moves: neighbours, pairs, halves of 8 and of 16 mirrored.
+constexpr int kSwap1 = 0xb1, kSwap2 = 0x4e, kHalfMirror = 0x141, kMirror = 0x140;
+
 // f (commutative, associative up to rounding) of all lanes' v, the same in every lane.
 template <class T, class F>
 __device__ __forceinline__ T over_lanes(T v, F f) {
   static_assert(sizeof(T) == 4 || sizeof(T) == 8, "one or two registers");
   constexpr int W = sizeof(T) / 4;
-  // data-parallel moves: neighbours, pairs, halves of 8 and of 16 mirrored
-  constexpr int kSwap1 = 0xb1, kSwap2 = 0x4e, kHalfMirror = 0x141, kMirror = 0x140;
   auto step = [&](auto move) {
     uint32_t w[W], m[W];
     __builtin_memcpy(w, &v, sizeof(T));

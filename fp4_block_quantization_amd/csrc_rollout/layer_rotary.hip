@@ -15,7 +15,9 @@ namespace fp4q {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int64_t kWanted = 262144;  // threads: a wavefront for each of the chip's 4096 places
+// Threads wanted, so that a token's angles serve few heads of many tokens: 8192 tokens of 40 heads of
+// 128 take 42.9 us with 131072, 31.3 with twice that, 29.1, and 28.4 with this many.
+constexpr int64_t kWanted = 1048576;
 
 struct Params {
   const char* in[2];

@@ -118,8 +118,8 @@ FP4Q_API int64_t prompt_attention_workspace_bytes(int64_t q_tokens, int64_t q_he
  *   weight  the chosen score, with renormalize divided by the sum of the chosen
  *           scores (0 where that is 0), times scale
  *
- * Keys with a bias, and marks, are compared in FP64.  A NaN key ranks behind every
- * other, and the weights of a token with a NaN logit may be NaN; the chosen
+ * Keys with a bias, and marks, are formed in FP64 and compared to 42 bits behind
+ * the leading one.  A NaN key ranks behind every other, and the weights of a token with a NaN logit may be NaN; the chosen
  * experts are always distinct and in range.  A token whose logits are all
  * -infinity has weights of 0 (softmax).
  *
