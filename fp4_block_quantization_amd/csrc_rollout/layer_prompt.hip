@@ -400,13 +400,15 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
     // whole has one, it is left out here and added behind the loop.
     bool dirty = false;
     if (masked(step)) {
+      // an exponent of ones overflows to the sign when one is added to it
       uint32_t bad = 0;
 #pragma unroll 4
       for (int i = lane * 16; i < kKeys * kRow; i += 1024) {
         const uint4v u = *(const uint4v*)(t + i);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) bad |= finite_part(u[x]) ^ u[x];
+        for (int x = 0; x < 4; ++x) bad |= (u[x] & 0x7f807f80u) + 0x00800080u;
       }
+      bad &= 0x80008000u;
       dirty = __any(bad != 0);
     }
     if (dirty) {
@@ -488,44 +490,31 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
   };
   const int own_steps = min((wave_limit + kKeys - 1) / kKeys, steps);  // this wavefront's end
   const int whole_steps = min(all_see / kKeys, steps);  // end of those that all its rows see whole
-  float16v sc[2];
-  begin();
-  copy_pair(step);
-  if (step < own_steps) score(step, sc);
-  // (while the pair that is copied meanwhile exists to its last key)
-  const int full_steps = min(whole_steps - 1, min(steps, s.n / kKeys) - 2);
-#pragma unroll 1
-  for (; step < full_steps && !large; ++step) {
-    float16v next[2];
-    begin();
-    const auto values = source(v_base, v_row, step + 1);
-    const auto keys = source(k_base, k_row, step + 2);
-    both(step, sc, next, [&](int n) {
-      if (n < kLoads)
-        copy_one(n, step + 1, values, v_row, v_from, tiles.v);
-      else if (n < 2 * kLoads)
-        copy_one(n - kLoads, step + 2, keys, k_row, k_from, tiles.k);
-    });
-    sc[0] = next[0];
-    sc[1] = next[1];
-  }
   const int last_whole = kMaskNext ? min(whole_steps, own_steps - 1) : whole_steps - 1;
+  // (one copy of the code of each kind of step: a workgroup of few steps waits for instructions)
+  const int full_steps = min(steps, s.n / kKeys) - 2;  // the pairs behind exist to their last key
+  float16v sc[2];
 #pragma unroll 1
-  for (; step < last_whole && !large; ++step) {
-    float16v next[2];
+  for (--step; step < steps; ++step) {
     begin();
     copy_pair(step + 1);
-    both(step, sc, next, [](int) {});
-    sc[0] = next[0];
-    sc[1] = next[1];
-  }
-#pragma unroll 1
-  for (; step < steps; ++step) {
-    begin();
-    copy_pair(step + 1);
-    if (step >= own_steps) continue;
-    add_values(step, sc);
+    if (step >= begin_step && step < own_steps) add_values(step, sc);
     if (step + 1 < own_steps) score(step + 1, sc);
+#pragma unroll 1
+    for (; step + 1 < min(full_steps, last_whole) && !large; ++step) {
+      float16v next[2];
+      begin();
+      const auto values = source(v_base, v_row, step + 2);
+      const auto keys = source(k_base, k_row, step + 3);
+      both(step + 1, sc, next, [&](int n) {
+        if (n < kLoads)
+          copy_one(n, step + 2, values, v_row, v_from, tiles.v);
+        else if (n < 2 * kLoads)
+          copy_one(n - kLoads, step + 3, keys, k_row, k_from, tiles.k);
+      });
+      sc[0] = next[0];
+      sc[1] = next[1];
+    }
   }
 
   if (any_dirty) {
@@ -567,14 +556,23 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
     return;
   }
   const float each = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t* to = p.out + row * D + 4 * half;
+  // the two halves hold every other four elements: exchanged, a lane has eight neighbours
+  uint16_t* to = p.out + row * D + 8 * half;
 #pragma unroll
   for (int d = 0; d < DT; ++d)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint2v u = {pack(o[d][4 * i] * each, o[d][4 * i + 1] * each),
-                        pack(o[d][4 * i + 2] * each, o[d][4 * i + 3] * each)};
-      *(uint2v*)(to + d * 32 + i * 8) = u;
+    for (int i = 0; i < 4; i += 2) {
+      uint4v u;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int e = 4 * i + 2 * x;
+        const auto r = __builtin_amdgcn_permlane32_swap(
+            pack(o[d][e] * each, o[d][e + 1] * each),
+            pack(o[d][e + 4] * each, o[d][e + 5] * each), false, false);
+        u[x] = r[0];
+        u[2 + x] = r[1];
+      }
+      *(uint4v*)(to + d * 32 + i * 8) = u;
     }
   if (p.lse && half == 0)
     p.lse[row] = l == 0.0f ? -INFINITY : (mc + __builtin_amdgcn_logf(l)) * kLn2;
