@@ -425,7 +425,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
   // operands two instructions ahead.
   auto both = [&](int step, float16v (&sc)[2], float16v (&next)[2], auto copies) {
     constexpr int kSlots = 2 * NK;  // matrix instructions of a half (4 * DT as well)
-    constexpr int kAhead = 2;
+    constexpr int kAhead = 3;
     const uint8_t *kt = tiles.k[(step + 1) & 1], *vt = tiles.v[step & 1];
     uint4v weights[4];
     auto probability = [&](int i) {
@@ -442,11 +442,14 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
     };
     bf16x8 ring[kAhead + 1];
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) ring[n] = fetch(n);
+    for (int n = 0; n < 2; ++n) ring[n] = fetch(n);
     next[0] = next[1] = (float16v)0.0f;
 #pragma unroll
     for (int n = 0; n < kSlots; ++n) {
-      ring[(n + kAhead) % (kAhead + 1)] = fetch(n + kAhead);
+      if (n % 2 == 0) {
+        ring[(n + 2) % 4] = fetch(n + 2);
+        ring[(n + 3) % 4] = fetch(n + 3);
+      }
       next[n % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[n % (kAhead + 1)], q[n / 2],
                                                             next[n % 2], 0, 0, 0);
       copies(n);
