@@ -19,7 +19,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kChunk = 2048;       // choices of a workgroup that counts or places
+constexpr int kPass = 1024;         // choices that a workgroup counts or places at a time
+constexpr int kMaxChunks = 256;     // workgroups of a call: every one reads all their counts
 constexpr int64_t kFew = 4096;     // choices up to which one launch does everything
 constexpr int kMaxExperts = 1024, kMaxChoices = 64;
 constexpr int64_t kLastLevel = 256 << 20;  // bytes of the cache in front of memory
@@ -35,7 +36,8 @@ struct Params {
   int32_t* counts;  // [chunks][experts]
   int64_t hidden;
   Divisor top_k;
-  int32_t entries, experts, chunks;
+  int32_t entries, experts;
+  int32_t chunks, chunk;  // and the choices of one, whole passes
   int64_t tokens;
 };
 
@@ -136,8 +138,9 @@ __global__ __launch_bounds__(kThreads) void count_chunks(const Params p) {
   const int tid = threadIdx.x;
   for (int e = tid; e < p.experts; e += kThreads) count[e] = 0;
   __syncthreads();
-  const int lo = blockIdx.x * kChunk, hi = min(lo + kChunk, p.entries);
-  for (int i = lo + tid; i < hi; i += kThreads) {
+  const int64_t lo = (int64_t)blockIdx.x * p.chunk;
+  const int64_t hi = min(lo + p.chunk, (int64_t)p.entries);
+  for (int64_t i = lo + tid; i < hi; i += kThreads) {
     const int e = p.chosen[i];
     if ((uint32_t)e < (uint32_t)p.experts) atomicAdd(&count[e], 1);
   }
@@ -146,28 +149,27 @@ __global__ __launch_bounds__(kThreads) void count_chunks(const Params p) {
     p.counts[(int64_t)blockIdx.x * p.experts + e] = count[e];
 }
 
-// Places of a chunk's choices.  A wavefront takes a quarter of them, 64 at a time in order;
-// next[wave][e] is the place of the next choice of e that the wavefront meets.
+// Places of a chunk's choices, a pass at a time.  A wavefront takes a quarter of a pass, 64 at a
+// time in order; next[wave][e] is the place of the next choice of e that the wavefront meets, and
+// base[e] that of the pass.
 __global__ __launch_bounds__(kThreads) void place_chunks(const Params p) {
   __shared__ int base[kMaxExperts], next[kWaves][kMaxExperts], sums[kWaves];
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, chunk = blockIdx.x;
-  int mine[kMaxExperts / kThreads];  // of the experts tid, tid + kThreads, ..: in chunks before
+  constexpr int kEach = kMaxExperts / kThreads;  // experts of a thread: tid, tid + kThreads, ..
+  int before[kEach];                             // their choices in chunks before
 #pragma unroll
-  for (int j = 0; j < kMaxExperts / kThreads; ++j) {
+  for (int j = 0; j < kEach; ++j) {
     const int e = j * kThreads + tid;
-    mine[j] = 0;
+    before[j] = 0;
     if (e >= p.experts) continue;
-    int all = 0, before = 0;
-#pragma unroll 8
+    int all = 0;
+#pragma unroll 32
     for (int c = 0; c < p.chunks; ++c) {
       const int n = p.counts[(int64_t)c * p.experts + e];
       all += n;
-      before += c < chunk ? n : 0;
+      before[j] += c < chunk ? n : 0;
     }
     base[e] = all;
-    mine[j] = before;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) next[w][e] = 0;
   }
   __syncthreads();
   const int all = scan_counts(base, p.experts, sums);
@@ -175,52 +177,67 @@ __global__ __launch_bounds__(kThreads) void place_chunks(const Params p) {
     for (int e = tid; e < p.experts; e += kThreads) p.offsets[e] = base[e];
     if (tid == 0) p.offsets[p.experts] = all;
   }
-  constexpr int kShare = kChunk / kWaves, kRounds = kShare / 64;
-  const int lo = chunk * kChunk + wave * kShare;
-  int own[kRounds];
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const int i = lo + r * 64 + lane;
-    own[r] = i < p.entries ? p.chosen[i] : -1;
-    if ((uint32_t)own[r] >= (uint32_t)p.experts) own[r] = -1;
-    if (own[r] >= 0) atomicAdd(&next[wave][own[r]], 1);
-  }
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kMaxExperts / kThreads; ++j) {
+  for (int j = 0; j < kEach; ++j) {
     const int e = j * kThreads + tid;
-    if (e >= p.experts) continue;
-    int at = base[e] + mine[j];
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const int n = next[w][e];
-      next[w][e] = at;
-      at += n;
-    }
+    if (e < p.experts) base[e] += before[j];
   }
-  __syncthreads();
   const int bits = 32 - __builtin_clz(p.experts);  // experts, and one number for none
+  const int64_t from = (int64_t)chunk * p.chunk;
+  const int64_t to = min(from + p.chunk, (int64_t)p.entries);
+  for (int64_t pass = from; pass < to; pass += kPass) {
+    __syncthreads();  // (the pass before is done with its places)
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const int i = lo + r * 64 + lane;
-    const int e = own[r] >= 0 ? own[r] : p.experts;
-    uint64_t peers = ~0ull;  // lanes with the same expert
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t set = __ballot((e >> b) & 1);
-      peers &= (e >> b) & 1 ? set : ~set;
+    for (int j = 0; j < kEach; ++j) {
+      const int e = j * kThreads + tid;
+      if (e < p.experts)
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) next[w][e] = 0;
     }
-    int at = -1;
-    if (own[r] >= 0) {
-      const int ahead = __popcll(peers & ((1ull << lane) - 1));
-      at = next[wave][e] + ahead;
+    __syncthreads();
+    constexpr int kShare = kPass / kWaves, kRounds = kShare / 64;
+    const int64_t lo = pass + wave * kShare + lane;
+    int own[kRounds];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      own[r] = lo + r * 64 < to ? p.chosen[lo + r * 64] : -1;
+      if ((uint32_t)own[r] >= (uint32_t)p.experts) own[r] = -1;
+      if (own[r] >= 0) atomicAdd(&next[wave][own[r]], 1);
     }
-    // every lane has read its expert's number before the first of them moves it on
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if (own[r] >= 0 && (peers >> lane) == 1) next[wave][e] = at + 1;  // (the last of them)
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if (i < p.entries) p.place[i] = at;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int e = j * kThreads + tid;
+      if (e >= p.experts) continue;
+      int at = base[e];
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const int n = next[w][e];
+        next[w][e] = at;
+        at += n;
+      }
+      base[e] = at;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const int e = own[r] >= 0 ? own[r] : p.experts;
+      uint64_t peers = ~0ull;  // lanes with the same expert
+      for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot((e >> b) & 1);
+        peers &= (e >> b) & 1 ? set : ~set;
+      }
+      int at = -1;
+      if (own[r] >= 0) at = next[wave][e] + __popcll(peers & ((1ull << lane) - 1));
+      // every lane has read its expert's number before the last of them moves it on
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (own[r] >= 0 && (peers >> lane) == 1) next[wave][e] = at + 1;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (lo + r * 64 < to) p.place[lo + r * 64] = at;
+    }
   }
 }
 
@@ -313,11 +330,21 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const Sums p) {
   }
 }
 
+struct Chunks {
+  int64_t count, each;
+};
+
+Chunks chunks_of(int64_t entries) {
+  const int64_t passes = entries > 0 ? (entries + kPass - 1) / kPass : 1;
+  const int64_t each = (passes + kMaxChunks - 1) / kMaxChunks * kPass;
+  return Chunks{(entries + each - 1) / each, each};
+}
+
 }  // namespace
 
 int64_t dispatch_workspace_bytes(int64_t tokens, int64_t top_k, int64_t experts) {
   const int64_t entries = tokens * top_k;
-  return entries <= kFew ? 0 : (entries + kChunk - 1) / kChunk * experts * 4;
+  return entries <= kFew ? 0 : chunks_of(entries).count * experts * 4;
 }
 
 hipError_t dispatch_launch(const DispatchArgs& a, hipStream_t stream) {
@@ -332,7 +359,9 @@ hipError_t dispatch_launch(const DispatchArgs& a, hipStream_t stream) {
   p.top_k = divisor_of((uint32_t)a.top_k);
   p.entries = (int32_t)(a.tokens * a.top_k);
   p.experts = (int32_t)a.experts;
-  p.chunks = (int32_t)(((int64_t)p.entries + kChunk - 1) / kChunk);
+  const Chunks chunks = chunks_of(p.entries);
+  p.chunks = (int32_t)chunks.count;
+  p.chunk = (int32_t)chunks.each;
   p.tokens = a.tokens;
   const bool wide = a.hidden % 8 == 0 && ((uintptr_t)a.x | (uintptr_t)a.rows) % 16 == 0;
   const int64_t pieces = wide ? a.hidden / 8 : a.hidden;

@@ -42,7 +42,7 @@ def check(x, e, experts, got):
     assert torch.equal(rows[at].view(torch.int16), x[torch.from_numpy(token).cuda()].view(torch.int16))
 
 
-# up to 4096 choices in one launch, more in several; chunks of 2048
+# up to 4096 choices in one launch, more in several; passes of 1024
 @pytest.mark.parametrize("tokens,top_k", [(1, 1), (1, 64), (3, 5), (64, 8), (511, 8), (512, 8), (513, 8), (4097, 1),
                                           (700, 6), (64, 64), (2500, 7), (20000, 2)])
 @pytest.mark.parametrize("experts", [1, 2, 31, 64, 257, 1024])
@@ -59,6 +59,14 @@ def test_widths(hidden, tokens):
     e = choices(tokens, 4, 16)
     x = torch.randn((tokens, hidden), device="cuda").bfloat16()
     check(x, e, 16, fq.moe_dispatch(x, e, 16))
+
+
+def test_chunks_of_several_passes():
+    # more than 256 chunks of 1024 choices
+    for tokens, top_k, experts in ((150001, 2, 37), (400000, 1, 1024), (70000, 8, 8)):
+        e = choices(tokens, top_k, experts, padding=True, skew=3.0)
+        x = torch.arange(tokens, device="cuda").int().view(torch.bfloat16).view(tokens, 2)
+        check(x, e, experts, fq.moe_dispatch(x, e, experts))
 
 
 def test_all_to_one_expert_and_none():
