@@ -260,7 +260,7 @@ struct Sums {
   int32_t top_k;
 };
 
-template <class T, int N>
+template <class T, int N, bool ONCE = false>
 __device__ __forceinline__ void load_run(const char* base, int64_t at, float (&v)[N]) {
   if constexpr (N == 1) {
     v[0] = (float)((const T*)base)[at];
@@ -270,7 +270,8 @@ __device__ __forceinline__ void load_run(const char* base, int64_t at, float (&v
     typedef T vec __attribute__((ext_vector_type(E)));
 #pragma unroll
     for (int i = 0; i < N / E; ++i) {
-      const vec w = *(const vec*)((const T*)base + at + i * E);
+      const vec* from = (const vec*)((const T*)base + at + i * E);
+      const vec w = ONCE ? __builtin_nontemporal_load(from) : *from;
 #pragma unroll
       for (int j = 0; j < E; ++j) v[i * E + j] = (float)w[j];
     }
@@ -297,7 +298,7 @@ __device__ __forceinline__ void store_run(char* base, int64_t at, const float (&
 // A workgroup takes a token and a part of its columns; a thread N of them.  The rows of eight
 // choices are asked for at once (with a branch at
 // each, one at a time): a choice without a row reads row 0, and takes nothing of it.
-template <class T, class O, int N>
+template <class T, class O, int N, bool ONCE>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const Sums p) {
   constexpr int kBatch = 8;
   for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
@@ -317,7 +318,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const Sums p) {
           const int choice = min(j0 + j, p.top_k - 1), at = place[choice];
           has[j] = j0 + j < p.top_k && at >= 0 && at < p.y_rows;
           w[j] = weights[choice];
-          load_run<T, N>(p.y, (has[j] ? at : 0) * p.n + c, v[j]);
+          load_run<T, N, ONCE>(p.y, (has[j] ? at : 0) * p.n + c, v[j]);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j)
@@ -403,13 +404,20 @@ hipError_t combine_launch(const CombineArgs& a, hipStream_t stream) {
   const int64_t parts = (a.n / (wide ? 8 : 1) + kThreads - 1) / kThreads;
   const dim3 grid((uint32_t)(a.tokens < (1 << 20) ? a.tokens : (1 << 20)),
                   (uint32_t)(parts < 1 ? 1 : parts < 8 ? parts : 8));
+  // Rows that take a quarter of the last-level cache or more are read past it, so that they evict
+  // nothing: after the dispatch that wrote them, through the caches and past them, 67 MB 38.2 and
+  // 38.8 us, 117 MB 59.7 and 54.9, 268 MB 137 and 124; after another pass 48 and 41, 71 and 63, 136
+  // and 123.  7 MB, just written, 5.2 and 6.2 us.
+  const bool once = a.y_rows * a.n * (a.y_fp32 ? 4 : 2) >= kLastLevel / 4;
   auto go = [&](auto t, auto o) {
     using T = decltype(t);
     using O = decltype(o);
-    if (wide)
-      combine_kernel<T, O, 8><<<grid, kThreads, 0, stream>>>(p);
+    if (wide && once)
+      combine_kernel<T, O, 8, true><<<grid, kThreads, 0, stream>>>(p);
+    else if (wide)
+      combine_kernel<T, O, 8, false><<<grid, kThreads, 0, stream>>>(p);
     else
-      combine_kernel<T, O, 1><<<grid, kThreads, 0, stream>>>(p);
+      combine_kernel<T, O, 1, false><<<grid, kThreads, 0, stream>>>(p);
     return hipGetLastError();
   };
   if (a.y_fp32) return a.out_fp32 ? go(0.0f, 0.0f) : go(0.0f, __bf16{});
