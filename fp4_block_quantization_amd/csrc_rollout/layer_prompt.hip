@@ -425,7 +425,6 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
   // operands two instructions ahead.
   auto both = [&](int step, float16v (&sc)[2], float16v (&next)[2], auto copies) {
     constexpr int kSlots = 2 * NK;  // matrix instructions of a half (4 * DT as well)
-    constexpr int kAhead = 3;
     const uint8_t *kt = tiles.k[(step + 1) & 1], *vt = tiles.v[step & 1];
     uint4v weights[4];
     auto probability = [&](int i) {
@@ -440,18 +439,20 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
                         : __builtin_bit_cast(bf16x8, value_part(vt, (n - kSlots) / DT,
                                                                 (n - kSlots) % DT));
     };
-    bf16x8 ring[kAhead + 1];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) ring[n] = fetch(n);
+    bf16x8 ring[4];  // before an instruction of even number, the operands of the next pair
+    auto fetch_pair = [&](int n) {
+      if (n % 2 == 0 && n < 2 * kSlots) {
+        ring[n % 4] = fetch(n);
+        ring[n % 4 + 1] = fetch(n + 1);
+      }
+    };
+    fetch_pair(0);
     next[0] = next[1] = (float16v)0.0f;
 #pragma unroll
     for (int n = 0; n < kSlots; ++n) {
-      if (n % 2 == 0) {
-        ring[(n + 2) % 4] = fetch(n + 2);
-        ring[(n + 3) % 4] = fetch(n + 3);
-      }
-      next[n % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[n % (kAhead + 1)], q[n / 2],
-                                                            next[n % 2], 0, 0, 0);
+      fetch_pair(n + 2);
+      next[n % 2] =
+          __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[n % 4], q[n / 2], next[n % 2], 0, 0, 0);
       copies(n);
 #pragma unroll
       for (int i = n * 24 / kSlots; i < (n + 1) * 24 / kSlots; ++i) probability(i);
@@ -460,13 +461,10 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
     float top = next[0][0];
 #pragma unroll
     for (int n = 0; n < kSlots; ++n) {
-      constexpr int kAll = 2 * kSlots;
-      if (n + kSlots + kAhead < kAll)
-        ring[(n + kSlots + kAhead) % (kAhead + 1)] = fetch(n + kSlots + kAhead);
+      fetch_pair(n + kSlots + 2);
       const int j = n / DT, d = n % DT;
-      o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[(n + kSlots) % (kAhead + 1)],
-                                                     __builtin_bit_cast(bf16x8, weights[j]), o[d],
-                                                     0, 0, 0);
+      o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+          ring[n % 4], __builtin_bit_cast(bf16x8, weights[j]), o[d], 0, 0, 0);
       if (n < kSlots / 2) {
 #pragma unroll
         for (int i = 24 + n * 16 / kSlots; i < 24 + (n + 1) * 16 / kSlots; ++i) probability(i);
