@@ -123,10 +123,15 @@ __device__ __forceinline__ Block block_by_length(const Params& p, int w) {
   Sequence s{0, 0, 0, 0};
   if (lane < p.batch) s = sequence(p, lane);
   const int blocks = (int)(((uint32_t)s.m * p.per_head.d + kRows - 1) / kRows);
+  // (lanes without a sequence have no blocks)
   int before = 0;
-  for (int i = 0; i < p.batch; ++i) {
-    const int n = __builtin_amdgcn_readlane(s.n, i), c = __builtin_amdgcn_readlane(blocks, i);
-    before += n > s.n || (n == s.n && i < lane) ? c : 0;
+  for (int i0 = 0; i0 < p.batch; i0 += 8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j;
+      const int n = __builtin_amdgcn_readlane(s.n, i), c = __builtin_amdgcn_readlane(blocks, i);
+      before += n > s.n || (n == s.n && i < lane) ? c : 0;
+    }
   }
   const uint64_t is = __ballot(lane < p.batch && w >= before && w < before + blocks);
   if (is == 0) return Block{{0, 0, 0, 0}, -1};
@@ -493,7 +498,9 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
   const int whole_steps = min(all_see / kKeys, steps);  // end of those that all its rows see whole
   const int last_whole = kMaskNext ? min(whole_steps, own_steps - 1) : whole_steps - 1;
   // (one copy of the code of each kind of step: a workgroup of few steps waits for instructions)
-  const int full_steps = min(steps, s.n / kKeys) - 2;  // the pairs behind exist to their last key
+  // The pairs copied in the inner loop have to exist to their last key (behind the last step keys
+  // are copied as well, once more the last step's, and not used).
+  const int fast_end = min(last_whole, s.n / kKeys >= steps ? steps : s.n / kKeys - 2);
   float16v sc[2];
 #pragma unroll 1
   for (--step; step < steps; ++step) {
@@ -502,11 +509,11 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
     if (step >= begin_step && step < own_steps) add_values(step, sc);
     if (step + 1 < own_steps) score(step + 1, sc);
 #pragma unroll 1
-    for (; step + 1 < min(full_steps, last_whole) && !large; ++step) {
+    for (; step + 1 < fast_end && !large; ++step) {
       float16v next[2];
       begin();
       const auto values = source(v_base, v_row, step + 2);
-      const auto keys = source(k_base, k_row, step + 3);
+      const auto keys = source(k_base, k_row, min(step + 3, steps - 1));
       both(step + 1, sc, next, [&](int n) {
         if (n < kLoads)
           copy_one(n, step + 2, values, v_row, v_from, tiles.v);
