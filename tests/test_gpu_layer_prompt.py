@@ -111,6 +111,21 @@ def test_many_sequences():
             lu.check(got[b], o, bound, "length %d" % n)
 
 
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("lens", [[700, 3], [0, 400, 400, 1, 257], [5, 300, 0, 128, 300, 64, 299, 1, 512, 0, 128],
+                                  [(37 * i) % 90 for i in range(64)]])
+def test_more_blocks_than_run_at_once(lens, d):
+    # over 512 workgroups of up to 64 sequences: they go in order of length
+    q, k, v = inputs(lens, lens, 130, 130, d, seed=47, gain=1.5)
+    out, lse = fq.prompt_attention(q, k, v, offsets(lens), lse=True)
+    some = slice(0, 130, 43)
+    check(q[:, some], k[:, some], v[:, some], lens, lens, out[:, some], lse[:, some], label="by length")
+    # every head, the same keys for all: each as the first
+    kk, vv, qq = (t[:, :1].expand(-1, 130, -1).contiguous() for t in (k, v, q))
+    out = fq.prompt_attention(qq, kk, vv, offsets(lens))
+    assert torch.equal(out, out[:, :1].expand(-1, 130, -1))
+
+
 def test_one_sequence_alone_is_the_same_as_packed():
     lens = [300, 17, 129]
     q, k, v = inputs(lens, lens, 8, 2, 128, seed=13)

@@ -174,6 +174,19 @@ def test_there_and_back():
         assert torch.allclose(back, x.float(), rtol=1e-5, atol=1e-6)
 
 
+def test_rows_that_the_caches_do_not_hold():
+    # 256 MiB and more there, 64 MiB and more back; a choice in five without a row
+    tokens, top_k, experts, hidden = 4500, 2, 9, 16384
+    e = choices(tokens, top_k, experts, padding=True)
+    x = torch.randn((tokens, hidden), device="cuda").bfloat16()
+    rows, off, place = fq.moe_dispatch(x, e, experts)
+    check(x, e, experts, (rows, off, place))
+    # weights that are powers of two: the sums are exact but for one rounding
+    w = torch.tensor([0.5, 2.0], device="cuda").expand(tokens, 2).contiguous()
+    want = sum(w[:, j:j + 1] * (place[:, j:j + 1] >= 0) * x.float() for j in range(2)).bfloat16()
+    assert torch.equal(fq.moe_combine(rows, place, w), want)
+
+
 def test_past_32_bit_offsets():
     # rows beyond 2^31 elements
     tokens, top_k, hidden = 70, 8, 1 << 22
