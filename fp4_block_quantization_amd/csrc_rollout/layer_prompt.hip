@@ -5,10 +5,12 @@
 // a row's running maximum of its scores s:
 //   p = 2^(s c - m c), l += p, O += p v;  out = O / l, lse = (m c + log2 l) ln 2
 // m is moved only when a score passes it by 8 / c: until then p is at most
-// 2^8, and BF16 holds that as well as 1.  p enters the value product in BF16
-// (8 bits, as the output has: a row's errors, 2^-9 each at most, are averaged
-// over its keys); s, m, l and O are FP32.  Where |m c| passes 2^20, s c - m c
-// is formed as (s - m) c, which does not cancel.
+// 2^8, and BF16 holds that as well as 1, while a move costs a pass over O.  p
+// enters the value product in BF16, as the operands of the matrix instruction
+// are (half a step is 2^-8 of it or less, and a row's errors are averaged over
+// its keys); s, m, l and O are FP32, and l sums p before it is rounded.  Where
+// |m c| passes 2^20, s c - m c would lose more than 2^-4 to cancellation and is
+// formed as (s - m) c, in steps of their own.
 //
 // Layout.  Scores are computed transposed, S^T = K Q^T (32 x 32 x 16 matrix
 // instructions): a lane holds 16 keys' scores of one query of every 32 keys,
@@ -16,16 +18,35 @@
 // the wavefront, and the probabilities of 16 keys, rounded to BF16, are the
 // operand of O^T = V^T P^T as they lie when the values' keys are taken in the
 // same order; the LDS's transposing read turns the values.  Keys and values go
-// to LDS without passing registers, 64 keys a step, two steps in flight, their
-// 16-byte pieces permuted within 128 bytes so that neither read has bank
-// conflicts.
+// to LDS without passing registers, 64 keys a step, in two tiles each: while a
+// step's keys or values are read the next one's arrive.  Their 16-byte pieces
+// are permuted within 128 bytes so that neither read has bank conflicts.
 //
 // Work.  A workgroup takes the rows (query, head of those that share a key
 // head) of one sequence and key head, 32 a wavefront: the heads that share
 // keys share their loads as well, and few queries fill a tile.  Workgroup
 // numbers run over key heads first, so that a key head's workgroups meet in
-// the same dies' L2, and the last rows of a sequence, which see the most keys,
-// start first.
+// the same dies' L2.  The last rows of a sequence, which see the most keys,
+// start first, and the longest sequences where there are workgroups that wait;
+// few rows behind many keys are cut along the keys and joined by a second
+// kernel (parts_of).
+//
+// Bounds.  A step of 32 rows by 64 keys of 128 is 32 matrix instructions of 32
+// cycles and, of every lane, 32 scores at about 22 cycles of vector work (an
+// exponential is 8).  `both` places the one beside the other by hand; a step
+// then takes a wavefront 3150 cycles, two of which share a SIMD: 1575 for the
+// 1024 of matrix work, at the 1.5 to 1.8 GHz that the chip runs at in this
+// kernel.  One sequence of 8192 tokens, 32 heads on 8 of 128: 525 us, 1045
+// TFLOP/s, where a large product of the library reaches 1380.  There is one
+// copy of the code of each kind of step, for a workgroup of few steps waits for
+// its instructions from memory: 16 sequences of up to 2048 tokens took 273 us
+// with the steps written out and 250 now, 770 TFLOP/s.  There four tenths of a
+// workgroup's time go outside whole steps: its block's search, the first copies
+// and the queries, three steps one after the other, the output.
+// Measured and not taken, for 8192 tokens when this took 530 us: 64 rows a
+// wavefront 615 us (its accumulators pass through the other half of the
+// registers), two wavefronts that share rows and take every other step 635,
+// three steps' copies in flight 695.
 #include <algorithm>
 #include <cmath>
 
@@ -47,7 +68,7 @@ constexpr int kWaves = 4, kRows = 32 * kWaves;  // of a workgroup
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kSlack = 8.0f;       // powers of two by which scores may pass m
-constexpr float kLarge = 0x1p20f;
+constexpr float kLarge = 0x1p20f;    // |m c| from which exponents are formed as (s - m) c
 
 // The same value in every lane, said so.
 __device__ __forceinline__ int32_t same(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -91,8 +112,8 @@ struct Block {
   int block;
 };
 
-// Blocks in the sequences' order: sequence b's are numbered from q_offsets[b] * per_head /
-// kRows + b on, which leaves room for all of them: rows / kRows, rounded up, is at most one more than the
+// Blocks in the sequences' order: sequence b's are numbered from q_offsets[b] * per_head / kRows +
+// b on, which leaves room for all of them: rows / kRows, rounded up, is at most one more than the
 // difference of that quotient.
 __device__ __forceinline__ Block block_by_place(const Params& p, int w) {
   const int lane = threadIdx.x % 64;
@@ -223,7 +244,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
   const int share = (int)quotient((uint32_t)all_steps + p.parts.d - 1, p.parts);
   const int begin_step = part * share, steps = min(begin_step + share, all_steps);
 
-  // A step's copies: this wavefront's keys are the 16 from wave * 16 on, D / 64 copies for every eight; the pieces' order comes again with these.
+  // A step's copies: this wavefront's keys are the 16 from wave * 16 on, D / 64 copies for every
+  // eight of them; the pieces' order comes again with these.
   constexpr int kPeriod = D / 64, kLoads = kKeys / kWaves / 8 * kPeriod;
   const char* k_base = (const char*)(p.k + (int64_t)s.k0 * p.k_stride + kvh * D);
   const char* v_base = (const char*)(p.v + (int64_t)s.k0 * p.v_stride + kvh * D);

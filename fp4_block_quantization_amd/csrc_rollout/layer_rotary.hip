@@ -8,6 +8,11 @@
 // Work.  A thread owns some pairs of one token (16 bytes of a head, or two
 // times 16 where the halves lie apart), computes their sines and cosines once
 // and applies them to every HS-th head of the queries and keys.
+//
+// Bounds.  Every element is read and written once: 8192 tokens of 40 heads of
+// 128 are 168 MB, 28.4 us, 5.9 TB/s, where a large copy reaches 5.6 to 6.4.
+// 64 tokens take 2.9 us on the device, of which a launch that does nothing is
+// 2.4.
 #include "layer_launch.h"
 #include "rollout_divisor.h"
 
@@ -15,8 +20,8 @@ namespace fp4q {
 namespace {
 
 constexpr int kThreads = 256;
-// Threads wanted, so that a token's angles serve few heads of many tokens: 8192 tokens of 40 heads of
-// 128 take 42.9 us with 131072, 31.3 with twice that, 29.1, and 28.4 with this many.
+// Threads wanted, so that a token's angles serve few heads of many tokens: 8192 tokens of 40 heads
+// of 128 take 42.9 us with 131072, 31.3 with twice that, 29.1, and 28.4 with this many.
 constexpr int64_t kWanted = 1048576;
 
 struct Params {
