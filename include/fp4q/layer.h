@@ -111,17 +111,17 @@ FP4Q_API int64_t prompt_attention_workspace_bytes(int64_t q_tokens, int64_t q_he
  *           order, unrounded).  The bias has no part in the weights.
  *   groups  above 1: experts are in that many equal groups of neighbours, a
  *           group's mark is the sum of the two largest keys in it (without a
- *           bias: scores; of the one, in groups of one), and only the experts of the top_groups groups with
- *           the largest marks can be chosen
+ *           bias: scores; of the one, in groups of one), and only the experts
+ *           of the top_groups groups with the largest marks can be chosen
  *   chosen  the top_k largest keys, in falling order; of equal keys or marks
  *           the lower index comes first
  *   weight  the chosen score, with renormalize divided by the sum of the chosen
  *           scores (0 where that is 0), times scale
  *
  * Keys with a bias, and marks, are formed in FP64 and compared to 42 bits behind
- * the leading one.  A NaN key ranks behind every other, and the weights of a token with a NaN logit may be NaN; the chosen
- * experts are always distinct and in range.  A token whose logits are all
- * -infinity has weights of 0 (softmax).
+ * the leading one.  A NaN key ranks behind every other, and the weights of a
+ * token with a NaN logit may be NaN; the chosen experts are always distinct and
+ * in range.  A token whose logits are all -infinity has weights of 0 (softmax).
  *
  *   logits   BF16 (fp32 0) or float (1) [tokens, experts], aligned to an element.
  *   tokens   0 ... 2^30; experts 1 ... 1024; top_k 1 ... 64, at most
