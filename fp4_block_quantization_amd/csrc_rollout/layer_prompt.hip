@@ -167,11 +167,10 @@ __device__ __forceinline__ Block block_by_length(const Params& p, int w) {
 // reads.  Nothing is returned to registers; the callers wait for vmcnt before the tiles are read.
 // m0 holds nothing of the compiler's here.)
 __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t base, uint32_t lane, uint32_t scalar,
-                                       uint8_t* lds) {
-  const uint32_t at = (uint32_t)same((int32_t)(uint32_t)(uintptr_t)(lds_void*)lds);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                                       uint32_t lds) {
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
-               : "s"(at), "v"(lane), "s"(base), "s"(scalar)
+               : "{m0}"(lds), "v"(lane), "s"(base), "s"(scalar)
                : "memory");
 }
 
@@ -264,23 +263,30 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
     k_from[n] = key * k_row + in_row;
     v_from[n] = key * v_row + in_row;
   }
-  auto source = [&](const char* base, uint32_t row, int step) {
-    return __builtin_amdgcn_make_buffer_rsrc((void*)(base + (int64_t)step * kKeys * row), 0, -1,
-                                             0x20000);
+  auto buffer = [&](const char* at) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)at, 0, -1, 0x20000);
   };
-  auto copy_one = [&](int n, int step, __amdgpu_buffer_rsrc_t at, uint32_t row,
-                      const uint32_t (&from)[kPeriod], uint8_t (&tile)[2][kKeys * D * 2]) {
-    to_lds(at, from[n % kPeriod], n / kPeriod * 8 * row,
-           tile[step & 1] + (wave * kLoads + n) * 1024);
+  auto source = [&](const char* base, uint32_t row, int step) {
+    return buffer(base + (int64_t)step * kKeys * row);
+  };
+  // (offsets in LDS as numbers: a generic pointer is checked for null at every copy)
+  constexpr uint32_t kTile = kKeys * D * 2;
+  const uint32_t own_k = (uint32_t)same((int32_t)(uint32_t)(uintptr_t)(lds_void*)tiles.k) +
+                         wave * kLoads * 1024;
+  const uint32_t own_v = own_k + (uint32_t)offsetof(Tiles<D>, v);
+  auto copy_one = [&](int n, uint32_t to, __amdgpu_buffer_rsrc_t at, uint32_t row,
+                      const uint32_t (&from)[kPeriod]) {
+    to_lds(at, from[n % kPeriod], n / kPeriod * 8 * row, to + n * 1024);
   };
   // a step's keys (or values) to tile step % 2
   auto copy = [&](int step, const char* base, uint32_t row, const uint32_t (&from)[kPeriod],
-                  uint8_t (&tile)[2][kKeys * D * 2]) {
+                  uint32_t tile) {
     if (step >= steps) return;
     const auto at = source(base, row, step);
+    const uint32_t to = tile + (step & 1) * kTile;
     if (step * kKeys + kKeys <= s.n) {
 #pragma unroll
-      for (int n = 0; n < kLoads; ++n) copy_one(n, step, at, row, from, tile);
+      for (int n = 0; n < kLoads; ++n) copy_one(n, to, at, row, from);
     } else {
       // keys past the sequence's end are its last once more
 #pragma unroll 1
@@ -289,18 +295,18 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
         uint32_t in_row;
         piece_of(n, key, in_row);
         to_lds(at, (uint32_t)min(key, s.n - 1 - step * kKeys) * row + in_row, 0,
-               tile[step & 1] + (wave * kLoads + n) * 1024);
+               to + n * 1024);
       }
     }
   };
   // Copies go in pairs, a step's values and the next one's keys, one step ahead.
   auto copy_pair = [&](int step) {
-    copy(step, v_base, v_row, v_from, tiles.v);
-    copy(step + 1, k_base, k_row, k_from, tiles.k);
+    copy(step, v_base, v_row, v_from, own_v);
+    copy(step + 1, k_base, k_row, k_from, own_k);
   };
 
   int step = begin_step;
-  copy(step, k_base, k_row, k_from, tiles.k);
+  copy(step, k_base, k_row, k_from, own_k);
   // queries, as the scores' second operand
   bf16x8 q[NK];
   {
@@ -376,7 +382,19 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
     for (int i = 1; i < 32; ++i) top = __builtin_fmaxf(top, sc[i / 16][i % 16]);
     return top;
   };
-  // a step's scores, masked, and m for them
+  // scores to the exponents of their probabilities
+  auto exponents = [&](const float16v (&sc)[2], float16v (&to)[2]) {
+    if (large) {
+      const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) to[i / 16][i % 16] = (sc[i / 16][i % 16] - base) * p.c;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        to[i / 16][i % 16] = __builtin_fmaf(sc[i / 16][i % 16], p.c, -mc);
+    }
+  };
+  // a step's scores, masked, m for them, and the exponents
   auto score = [&](int step, float16v (&sc)[2]) {
     const uint8_t* t = tiles.k[step & 1];
 #pragma unroll
@@ -388,21 +406,13 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
     }
     if (masked(step)) mask(step, sc);
     renew(largest(sc));
+    exponents(sc, sc);
   };
-  // a step's probabilities and their product with the values
+  // a step's probabilities, from their exponents, and their product with the values
   auto add_values = [&](int step, float16v (&sc)[2]) {
     const uint8_t* t = tiles.v[step & 1];
-    if (large) {
-      const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        sc[i / 16][i % 16] = __builtin_amdgcn_exp2f((sc[i / 16][i % 16] - base) * p.c);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        sc[i / 16][i % 16] =
-            __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i / 16][i % 16], p.c, -mc));
-    }
+    for (int i = 0; i < 32; ++i) sc[i / 16][i % 16] = __builtin_amdgcn_exp2f(sc[i / 16][i % 16]);
 #pragma unroll
     for (int i = 0; i < 32; ++i) l += sc[i / 16][i % 16];
     uint4v weights[4];  // 16 keys each
@@ -446,21 +456,25 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
       product(std::false_type{});
     }
   };
-  // Both at once, add_values(step, sc) and score(step + 1, next), for a step that every row sees
-  // whole: the matrix units do the next step's scores, then this one's values, and beside each of
-  // their instructions stand a few of the others' -- the probabilities in the first half (the
-  // last quarter in the second), the next step's maximum in the second -- and the reads of
-  // operands two instructions ahead.
+  // Both at once, add_values(step, sc) and score(step + 1, next) but for the exponents, for a step
+  // that every row sees whole: the matrix units do the next step's scores, then this one's values,
+  // and beside each of their instructions stand a few of the others' -- the probabilities in the
+  // first half (the last quarter in the second), the next step's maximum in the second -- and the
+  // reads of operands two instructions ahead.
   auto both = [&](int step, float16v (&sc)[2], float16v (&next)[2], auto copies) {
     constexpr int kSlots = 2 * NK;  // matrix instructions of a half (4 * DT as well)
     const uint8_t *kt = tiles.k[(step + 1) & 1], *vt = tiles.v[step & 1];
     uint4v weights[4];
+    auto packed = [&](int i) {  // (a pair later: what follows an exponential at once waits for it)
+      const float a = sc[i / 16][i % 16], b = sc[i / 16][i % 16 + 1];
+      l += a;
+      l += b;
+      weights[i / 8][i % 8 / 2] = pack(a, b);
+    };
     auto probability = [&](int i) {
-      const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i / 16][i % 16], p.c, -mc));
+      const float x = __builtin_amdgcn_exp2f(sc[i / 16][i % 16]);
+      if (i % 2 == 0 && i > 0) packed(i - 2);
       sc[i / 16][i % 16] = x;
-      l += x;
-      if (i % 2)
-        weights[i / 8][i % 8 / 2] = pack(sc[i / 16][i % 16 - 1], x);
     };
     auto fetch = [&](int n) {  // the operand of the n-th instruction of both halves
       return n < kSlots ? key_part(kt, n % 2, n / 2)
@@ -496,6 +510,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
       if (n < kSlots / 2) {
 #pragma unroll
         for (int i = 24 + n * 16 / kSlots; i < 24 + (n + 1) * 16 / kSlots; ++i) probability(i);
+        if (n == kSlots / 2 - 1) packed(30);
       } else {
 #pragma unroll
         for (int i = (n - kSlots / 2) * 64 / kSlots; i < (n + 1 - kSlots / 2) * 64 / kSlots; ++i)
@@ -531,20 +546,23 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
     copy_pair(step + 1);
     if (step >= begin_step && step < own_steps) add_values(step, sc);
     if (step + 1 < own_steps) score(step + 1, sc);
+    const char *v_from_step = v_base + (int64_t)(step + 2) * kKeys * v_row;
+    const char *k_from_step = k_base + (int64_t)min(step + 3, steps - 1) * kKeys * k_row;
 #pragma unroll 1
     for (; step + 1 < fast_end && !large; ++step) {
       float16v next[2];
       begin();
-      const auto values = source(v_base, v_row, step + 2);
-      const auto keys = source(k_base, k_row, min(step + 3, steps - 1));
+      const auto values = buffer(v_from_step), keys = buffer(k_from_step);
+      v_from_step += kKeys * v_row;
+      k_from_step += step + 4 < steps ? kKeys * k_row : 0;  // (the last step's once more)
+      const uint32_t to_v = own_v + (step & 1) * kTile, to_k = own_k + (step + 1 & 1) * kTile;
       both(step + 1, sc, next, [&](int n) {
         if (n < kLoads)
-          copy_one(n, step + 2, values, v_row, v_from, tiles.v);
+          copy_one(n, to_v, values, v_row, v_from);
         else if (n < 2 * kLoads)
-          copy_one(n - kLoads, step + 3, keys, k_row, k_from, tiles.k);
+          copy_one(n - kLoads, to_k, keys, k_row, k_from);
       });
-      sc[0] = next[0];
-      sc[1] = next[1];
+      exponents(next, sc);  // (to sc's registers, which saves a copy)
     }
   }
 
