@@ -33,20 +33,23 @@
 //
 // Bounds.  A step of 32 rows by 64 keys of 128 is 32 matrix instructions of 32
 // cycles and, of every lane, 32 scores at about 22 cycles of vector work (an
-// exponential is 8).  `both` places the one beside the other by hand; a step
-// then takes a wavefront 3150 cycles, two of which share a SIMD: 1575 for the
-// 1024 of matrix work, at the 1.5 to 1.8 GHz that the chip runs at in this
-// kernel.  One sequence of 8192 tokens, 32 heads on 8 of 128: 525 us, 1045
-// TFLOP/s, where a large product of the library reaches 1380.  There is one
-// copy of the code of each kind of step, for a workgroup of few steps waits for
-// its instructions from memory: 16 sequences of up to 2048 tokens took 273 us
-// with the steps written out and 250 now, 770 TFLOP/s.  There four tenths of a
-// workgroup's time go outside whole steps: its block's search, the first copies
-// and the queries, three steps one after the other, the output.
+// exponential is 8), 48 reads of LDS and some 90 scalar instructions.  `both`
+// places them beside one another by hand.  Counted for one sequence of 8192
+// tokens, 32 heads on 8 of 128 (507 to 525 us by card, 1085 to 1050 TFLOP/s, at
+// 1.8 GHz, which power leaves; a large product of the library reaches 1380): a
+// SIMD's matrix unit works 58% of the time, its vector unit 52, the LDS 58, and
+// some instruction starts in 80: with two wavefronts a SIMD it is the starts
+// that bound.  There is one copy of the code of each kind of step, for a
+// workgroup of few steps waits for its instructions from memory: 16 sequences
+// of up to 2048 tokens took 273 us with the steps written out, and take 240 now
+// (800 TFLOP/s).  There four tenths of a workgroup's time go outside whole
+// steps: its block's search, the first copies and the queries, three steps one
+// after the other, the output.
 // Measured and not taken, for 8192 tokens when this took 530 us: 64 rows a
 // wavefront 615 us (its accumulators pass through the other half of the
 // registers), two wavefronts that share rows and take every other step 635,
-// three steps' copies in flight 695.
+// three steps' copies in flight 695; at 508, workgroups that stay and take one
+// block after the other 524 (and the 16 sequences 257 for 240).
 #include <algorithm>
 #include <cmath>
 
