@@ -14,13 +14,16 @@
 // 64, and so on.  The best are taken one at a time: a maximum over the lane's
 // own and one over the lanes (data-parallel moves, no LDS).  Of 32-bit keys
 // the expert is found from ballots: with the number in 64 bits as well, 8192
-// tokens of 128 experts take 9.3 us instead of 6.6, and 64 tokens of 256
-// experts 3.9 instead of 3.5.
+// tokens of 128 experts take 6.9 us instead of 6.5.  64-bit keys are sorted in
+// each lane first, and of its best the upper half goes over the lanes; with
+// both halves of the lane's largest, 8192 tokens of 256 experts with a bias and
+// groups take 16.1 us instead of 13.5, 64 of them 6.0 instead of 5.8, and 8192
+// of 1024 with a bias 34 instead of 31 (22 instead of 26 for the one best).
 //
 // Bounds.  The chain of these steps, of which each of the best waits for the
 // one before: 64 tokens of 256 experts take 3.5 us on the device for 8 of
-// them, 2.4 for one (a launch that does nothing is about 2), 4.8 with a bias,
-// 6.0 with groups as well; 8192 tokens of 128 experts 6.6 us, of 4.7 MB.
+// them, 2.4 for one (a launch that does nothing is about 2), 4.7 with a bias,
+// 5.8 with groups as well; 8192 tokens of 128 experts 6.6 us, of 4.7 MB.
 #include "layer_lanes.h"
 #include "layer_launch.h"
 #include "rollout_divisor.h"
@@ -78,15 +81,39 @@ __device__ __forceinline__ int take_best(uint32_t (&key)[S], int lane) {
   for (int j = 0; j < S; ++j) key[j] = j * 64 + lane == expert ? 0 : key[j];
   return expert;
 }
+// A lane's keys into falling order (Batcher's network of merges).
+template <int S>
+__device__ __forceinline__ void sort_lane(uint64_t (&key)[S]) {
+#pragma unroll
+  for (int p = 1; p < S; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int i = 0; i + k < S; ++i) {
+        if (i < k % p || (i - k % p) / k % 2 != 0 || i / (2 * p) != (i + k) / (2 * p)) continue;
+        const uint64_t a = key[i], b = key[i + k];
+        key[i] = b > a ? b : a;
+        key[i + k] = b > a ? a : b;
+      }
+}
+
+// Takes the best out of sorted 64-bit keys.  The lower halves are looked at only where lanes'
+// upper ones are equal.
 template <int S>
 __device__ __forceinline__ int take_best(uint64_t (&key)[S], int) {
-  uint64_t top = key[0];
+  const uint32_t high = (uint32_t)(key[0] >> 32), low = (uint32_t)key[0];
+  const uint32_t top = over_lanes(high, larger<uint32_t>);
+  bool best = high == top;
+  uint64_t with = __ballot(best);
+  if (with & (with - 1)) {
+    const uint32_t most = over_lanes(best ? low : 0, larger<uint32_t>);
+    best = best && low == most;
+    with = __ballot(best);
+  }
 #pragma unroll
-  for (int j = 1; j < S; ++j) top = larger(key[j], top);
-  top = over_lanes(top, larger<uint64_t>);
-#pragma unroll
-  for (int j = 0; j < S; ++j) key[j] = key[j] == top ? 0 : key[j];
-  return (int)(kNumbers - 1 - ((uint32_t)top & (kNumbers - 1)));
+  for (int j = 0; j < S; ++j) key[j] = !best ? key[j] : j + 1 < S ? key[j + 1] : 0;
+  const uint32_t number = __builtin_amdgcn_readlane((int)low, __builtin_ctzll(with));
+  return (int)(kNumbers - 1 - (number & (kNumbers - 1)));
 }
 
 // The two largest of some numbers.
@@ -230,6 +257,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const Params p, cons
     else if constexpr (WIDE)
       key[j] |= kNumbers - 1 - e;
   }
+  if constexpr (WIDE) sort_lane(key);
   __shared__ float all[kWaves][S * 64];
 #pragma unroll
   for (int j = 0; j < S; ++j) all[wave][j * 64 + lane] = x[j];
