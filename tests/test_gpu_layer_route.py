@@ -151,6 +151,20 @@ def test_weights_that_underflow():
     assert e.tolist() == [[3, 2]] and w.tolist() == [[0.5, 0.5]]
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups,top_groups,top_k", [
+    (64, 1, 1, 9), (100, 1, 1, 64), (256, 1, 1, 10), (256, 8, 3, 33), (512, 1, 1, 64), (1024, 1, 1, 40),
+    (1024, 16, 5, 20)])
+def test_many_equal_keys_with_a_bias(experts, groups, top_groups, top_k, scoring):
+    # two logits and two biases: a few keys, many experts of each, in one lane and in several
+    g = torch.Generator(device="cuda").manual_seed(experts + groups)
+    x = torch.randint(0, 2, (21, experts), generator=g, device="cuda").float()
+    x[:3] = 0.5
+    bias = torch.randint(0, 2, (experts,), generator=g, device="cuda").float()
+    got = fq.moe_route(x, top_k, bias=bias, scoring=scoring, groups=groups, top_groups=top_groups)
+    check(x, got, top_k, bias, scoring, groups, top_groups, label="equal keys")
+
+
 def test_many_tokens():
     x = logits_of(5000, 96, torch.bfloat16)
     got = fq.moe_route(x, 4)
