@@ -106,6 +106,38 @@ struct Device {
   }
 };
 
+// Outputs of a call.  Small ones lie in one allocation: each costs a microsecond of the host's time,
+// of the five that a call takes.  (Larger ones do not keep each other's memory.)
+template <size_t N>
+void allocate(const Device& device, const at::IntArrayRef (&shapes)[N],
+              const at::ScalarType (&types)[N], at::Tensor* out) {
+  constexpr int64_t kTogether = 4 << 20, kAlign = 256;  // bytes
+  int64_t at[N], total = 0;
+  for (size_t i = 0; i < N && total <= kTogether; ++i) {
+    int64_t bytes = (int64_t)c10::elementSize(types[i]);
+    for (int64_t n : shapes[i]) {
+      if (n > kTogether || (bytes *= n) > kTogether) {
+        bytes = kTogether + 1;
+        break;
+      }
+    }
+    at[i] = total;
+    total += (bytes + kAlign - 1) / kAlign * kAlign;
+  }
+  if (total > kTogether) {
+    for (size_t i = 0; i < N; ++i) out[i] = device.empty(shapes[i], types[i]);
+    return;
+  }
+  const at::Tensor all = device.empty({total}, at::kByte);
+  for (size_t i = 0; i < N; ++i) {
+    out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                      c10::scalarTypeToTypeMeta(types[i]));
+    c10::TensorImpl* t = out[i].unsafeGetTensorImpl();
+    t->set_sizes_contiguous(shapes[i]);
+    t->set_storage_offset(at[i] / (int64_t)c10::elementSize(types[i]));
+  }
+}
+
 struct Workspace {
   at::Tensor held;
   void* data = nullptr;

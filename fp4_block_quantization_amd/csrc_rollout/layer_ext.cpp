@@ -105,10 +105,13 @@ PyObject* rotary(PyObject* const* arg) {
       no_gradient(out[i], out_names[i]);
       out_stride[i] = token_stride(out[i], out_names[i], heads[i], dim);
     } else {
-      out[i] = device.empty(t.sizes(), type);
       out_stride[i] = heads[i] * dim;
     }
   }
+  if (!given && in[1])
+    allocate(device, {in[0]->sizes(), in[1]->sizes()}, {type, type}, out);
+  else if (!given)
+    out[0] = device.empty(in[0]->sizes(), type);
   const at::Tensor& positions = sized(arg[2], "positions", at::kLong, tokens);
   const at::Tensor& frequencies = dense(arg[3], "frequencies", at::kDouble);
   if (frequencies.dim() != 1) refuse("frequencies must be [dims / 2]");
@@ -155,14 +158,18 @@ PyObject* prompt(PyObject* const* arg) {
   device.same(k_off);
   const double scale = arg[5] == Py_None ? 1.0 / std::sqrt((double)dim) : real(arg[5]);
   at::Tensor out[2];
-  if (arg[7] == Py_None) {
+  const bool lse = truth(arg[6]);
+  const int64_t lse_shape[] = {q_tokens, heads};
+  if (arg[7] == Py_None && lse) {
+    allocate(device, {q.sizes(), lse_shape}, {at::kBFloat16, at::kFloat}, out);
+  } else if (arg[7] == Py_None) {
     out[0] = device.empty(q.sizes(), at::kBFloat16);
   } else {
     out[0] = shaped(arg[7], "out", at::kBFloat16, q.sizes());
     device.same(out[0]);
     no_gradient(out[0], "out");
   }
-  if (truth(arg[6])) out[1] = device.empty({q_tokens, heads}, at::kFloat);
+  if (lse && !out[1].defined()) out[1] = device.empty(lse_shape, at::kFloat);
   const Workspace ws(
       arg[8],
       p_prompt_attention_workspace_bytes(q_tokens, heads, k_tokens, kv_heads, dim, batch), device);
@@ -202,8 +209,8 @@ PyObject* route(PyObject* const* arg) {
   if (top_k < 1) refuse("top_k must be at least 1");
   at::Tensor out[2];
   if (arg[9] == Py_None) {
-    out[0] = device.empty({tokens, top_k}, at::kFloat);
-    out[1] = device.empty({tokens, top_k}, at::kInt);
+    const int64_t shape[] = {tokens, top_k};
+    allocate(device, {shape, shape}, {at::kFloat, at::kInt}, out);
   } else {
     PyObject** given = parts_of(arg[9], 2, "(weights, experts)");
     out[0] = shaped(given[0], "weights", at::kFloat, {tokens, top_k});
@@ -234,9 +241,9 @@ PyObject* dispatch(PyObject* const* arg) {
   device.same(chosen);
   at::Tensor out[3];
   if (arg[3] == Py_None) {
+    const int64_t offsets[] = {experts + 1}, place[] = {tokens, top_k};
     out[0] = device.empty({tokens * top_k, hidden}, at::kBFloat16);
-    out[1] = device.empty({experts + 1}, at::kLong);
-    out[2] = device.empty({tokens, top_k}, at::kInt);
+    allocate(device, {offsets, place}, {at::kLong, at::kInt}, out + 1);
   } else {
     PyObject** given = parts_of(arg[3], 3, "(rows, offsets, place)");
     out[0] = shaped(given[0], "rows", at::kBFloat16, {tokens * top_k, hidden});

@@ -219,3 +219,34 @@ def test_inactive_padding_in_a_graph():
         assert int(off[-1]) == 4 * n and (place[n:] == -1).all() and (w[n:] == 0).all()
         assert (out[n:] == 0).all() and (rows[4 * n:] == 9).all()
         assert torch.equal(rows[place[:n].long()], x[:n, None].expand(n, 4, 64))
+
+
+def test_small_outputs_of_a_call_share_an_allocation_and_nothing_else():
+    f, _ = fq.rotary_frequencies(64)
+
+    def calls(tokens):
+        x = torch.randn((tokens, 6, 64), device="cuda").bfloat16()
+        p = torch.arange(tokens, device="cuda")
+        yield fq.rotary(x[:, :4], x[:, 4:], p, f)
+        yield fq.prompt_attention(x[:, :4], x[:, 4:5], x[:, 5:], torch.tensor([0, tokens], device="cuda").int(),
+                                  lse=True)
+        w, e = fq.moe_route(torch.randn((tokens, 9), device="cuda"), 3)
+        yield w, e
+        yield fq.moe_dispatch(x.view(tokens, 384), e, 9)[1:]
+
+    for tokens in (0, 1, 7, 300):
+        for outs in calls(tokens):
+            assert len({t.untyped_storage().data_ptr() for t in outs}) == 1
+            ends = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in outs if t.numel()]
+            assert all(a % 16 == 0 for a, _ in ends)
+            assert all(b <= c or d <= a for i, (a, b) in enumerate(ends) for c, d in ends[i + 1:])
+            assert all(t.is_contiguous() and not t.requires_grad and not t._is_view() for t in outs)
+            kept = [t.clone() for t in outs]
+            outs[0].fill_(3)
+            assert torch.equal(outs[1], kept[1])
+            outs[1].zero_()
+            assert (outs[0] == 3).all()
+    # larger ones do not keep each other's memory
+    q, k = next(calls(20000))
+    assert q.untyped_storage().data_ptr() != k.untyped_storage().data_ptr()
+    assert q.storage_offset() == k.storage_offset() == 0
