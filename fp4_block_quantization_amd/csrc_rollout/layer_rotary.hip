@@ -10,7 +10,7 @@
 // and applies them to every HS-th head of the queries and keys.
 //
 // Bounds.  Every element is read and written once: 8192 tokens of 40 heads of
-// 128 are 168 MB, 28.4 us, 5.9 TB/s, where a large copy reaches 5.6 to 6.4.
+// 128 are 168 MB, 28.9 us, 5.8 TB/s, where a large copy reaches 5.3 to 6.4.
 // 64 tokens take 2.9 us on the device, of which a launch that does nothing is
 // 2.4.
 #include "layer_launch.h"
@@ -88,11 +88,13 @@ template <class T, int N>
 struct Run {
   typedef T vec __attribute__((ext_vector_type(N)));
   T v[N];
+  // ONCE: past the caches
+  template <bool ONCE>
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (N == 1) {
       v[0] = *p;
     } else {
-      const vec w = *(const vec*)p;
+      const vec w = ONCE ? __builtin_nontemporal_load((const vec*)p) : *(const vec*)p;
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] = w[i];
     }
@@ -110,7 +112,8 @@ struct Run {
 };
 
 // WIDE: units of 16 bytes (two of them where halves lie apart); else of a pair, or an element.
-template <class T, bool WIDE, bool INTERLEAVED, bool INVERSE>
+// ONCE: inputs are read past the caches.
+template <class T, bool WIDE, bool INTERLEAVED, bool INVERSE, bool ONCE>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(const Params p) {
   using E = Element<T>;
   // elements of a run, and pairs of a unit
@@ -147,11 +150,11 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(const Params p) {
     if (!turns) {
       if (in == out) continue;
       Run<T, N> r;
-      r.load(in + first);
+      r.template load<ONCE>(in + first);
       r.store(out + first);
     } else if constexpr (WIDE && INTERLEAVED) {
       Run<T, N> r;
-      r.load(in + first);
+      r.template load<ONCE>(in + first);
 #pragma unroll
       for (int i = 0; i < PAIRS; ++i) {
         const float u = E::get(r.v[2 * i]), v = E::get(r.v[2 * i + 1]);
@@ -161,8 +164,8 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(const Params p) {
       r.store(out + first);
     } else {
       Run<T, N> a, b;
-      a.load(in + first);
-      b.load(in + second);
+      a.template load<ONCE>(in + first);
+      b.template load<ONCE>(in + second);
 #pragma unroll
       for (int i = 0; i < PAIRS; ++i) {
         const float u = E::get(a.v[i]), v = E::get(b.v[i]);
@@ -175,13 +178,20 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(const Params p) {
   }
 }
 
-template <class T, bool WIDE>
+template <class T, bool WIDE, bool ONCE>
 void* kernel_of(bool interleaved, bool inverse) {
   if (interleaved)
-    return inverse ? (void*)rotary_kernel<T, WIDE, true, true>
-                   : (void*)rotary_kernel<T, WIDE, true, false>;
-  return inverse ? (void*)rotary_kernel<T, WIDE, false, true>
-                 : (void*)rotary_kernel<T, WIDE, false, false>;
+    return inverse ? (void*)rotary_kernel<T, WIDE, true, true, ONCE>
+                   : (void*)rotary_kernel<T, WIDE, true, false, ONCE>;
+  return inverse ? (void*)rotary_kernel<T, WIDE, false, true, ONCE>
+                 : (void*)rotary_kernel<T, WIDE, false, false, ONCE>;
+}
+
+template <class T>
+void* kernel_of(bool wide, bool once, bool interleaved, bool inverse) {
+  return !wide ? kernel_of<T, false, false>(interleaved, inverse)
+         : once ? kernel_of<T, true, true>(interleaved, inverse)
+                : kernel_of<T, true, false>(interleaved, inverse);
 }
 
 }  // namespace
@@ -210,10 +220,13 @@ hipError_t rotary_launch(const RotaryArgs& a, hipStream_t stream) {
   const int64_t want = (kWanted + each - 1) / each, slots = want < all ? want : all;
   p.units = divisor_of((uint32_t)units);
   p.slots = divisor_of((uint32_t)slots);
-  void* kernel = a.fp32 ? (wide ? kernel_of<float, true>(a.interleaved, a.inverse)
-                                : kernel_of<float, false>(a.interleaved, a.inverse))
-                        : (wide ? kernel_of<__bf16, true>(a.interleaved, a.inverse)
-                                : kernel_of<__bf16, false>(a.interleaved, a.inverse));
+  // Inputs that take a quarter of the last-level cache or more are read past it, so that they evict
+  // nothing.  40 heads of 128, through the caches and past them: 8192 tokens 28.8 and 29.6 us where
+  // nothing else runs, 33.5 and 28.9 between other work, 37.0 and 34.5 in place; 16384 tokens 65
+  // and 54; 4096 tokens 16.5 and 17.1.
+  const bool once = a.tokens * all * a.head_dim * (a.fp32 ? 4 : 2) >= (int64_t)64 << 20;
+  void* kernel = a.fp32 ? kernel_of<float>(wide, once, a.interleaved, a.inverse)
+                        : kernel_of<__bf16>(wide, once, a.interleaved, a.inverse);
   const int64_t step = (((int64_t)1 << 31) - kThreads) / (units * slots);  // tokens of a launch
   for (p.first_token = 0; p.first_token < a.tokens; p.first_token += step) {
     const int64_t tokens = a.tokens - p.first_token < step ? a.tokens - p.first_token : step;

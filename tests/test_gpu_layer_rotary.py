@@ -102,6 +102,25 @@ def test_strided_in_place_and_out(dtype, pad, interleaved):
     assert torch.equal(qkv[:, (hq + 2 * hk) * d:], before[:, (hq + 2 * hk) * d:])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_many_tokens_are_as_few(dtype, interleaved, inverse):
+    # over 64 MiB at once, and in pieces below that
+    tokens = 9001
+    x = heads(tokens, 20, 192, dtype, 51)
+    f, a = fq.rotary_frequencies(64, method="parts", factor=8.0, original_positions=2048)
+    pos = positions_of(tokens, 100)
+    kw = dict(amplitude=a, interleaved=interleaved, inverse=inverse)
+    few = [fq.rotary(x[i:i + 1500, :16], x[i:i + 1500, 16:], pos[i:i + 1500], f, **kw) for i in range(0, tokens, 1500)]
+    want = torch.cat([q for q, _ in few]), torch.cat([k for _, k in few])
+    check(x[:50, :16], x[:50, 16:], pos[:50], f, a, interleaved, inverse, (want[0][:50], want[1][:50]), "few")
+    got = fq.rotary(x[:, :16], x[:, 16:], pos, f, **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    fq.rotary(x[:, :16], x[:, 16:], pos, f, out=(x[:, :16], x[:, 16:]), **kw)
+    assert torch.equal(x[:, :16], want[0]) and torch.equal(x[:, 16:], want[1])
+
+
 def test_inverse_is_the_transposed_map():
     # <rotary(x), y> = <x, rotary^T(y)>, with an amplitude; and against differences of the forward
     d, tokens = 32, 7
