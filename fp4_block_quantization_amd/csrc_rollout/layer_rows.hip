@@ -6,8 +6,8 @@
 // those of the same expert before it.  Whole numbers throughout, so the order
 // of additions does not matter; places are the same from call to call.
 //
-// Work.  Few choices: every workgroup counts them all and copies its token's
-// row, one launch.  Many: counts per chunk of choices; places from the counts
+// Work.  Few choices: every workgroup counts them all and copies its tokens'
+// rows, one launch.  Many: counts per chunk of choices; places from the counts
 // of the chunks before; then the rows, each token's read once and written to
 // its places.  The sums back read every row once.
 //
@@ -16,6 +16,8 @@
 // nothing is about 2.  Memory, when there are many: 8192 tokens of 8 rows of
 // 2048, 302 MB there and 336 back, take 120 us together, 5.3 TB/s, where a
 // large copy reaches 5.6 to 6.4; of these the places are 10 us.
+#include <algorithm>
+
 #include "layer_launch.h"
 #include "rollout_divisor.h"
 
@@ -27,8 +29,9 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kPass = 1024;         // choices that a workgroup counts or places at a time
 constexpr int kMaxChunks = 256;     // workgroups of a call: every one reads all their counts
 // Choices up to which one launch does everything: 512 tokens of 8 rows of 2048 take 8.4 us in one
-// and 13.6 in three, 64 of 7168 4.6 and 17.2; 1024 of 8 rows 16.7 and 17.2, 2048 31.5 and 24.0.
-constexpr int64_t kFew = 4096;
+// and 13.6 in three, 64 of 7168 4.7 and 17.2; 1024 of 8 rows 16.0 and 17.4, 4096 of one of 1024 8.3
+// and 11.3, 1024 of 8 11.0 and 14.2; 2048 of 8 rows 30.4 and 23.8.
+constexpr int64_t kFew = 8192;
 constexpr int kMaxExperts = 1024, kMaxChoices = 64;
 constexpr int64_t kLastLevel = 256 << 20;  // bytes of the cache in front of memory
 
@@ -46,6 +49,7 @@ struct Params {
   int32_t entries, experts;
   int32_t chunks, chunk;  // and the choices of one, whole passes
   int64_t tokens;
+  int32_t each;  // tokens of a workgroup, where one launch does everything
 };
 
 // counts[e] -> their sums before e, for threads of one workgroup; the sum of all is returned.
@@ -104,14 +108,17 @@ __device__ __forceinline__ void copy_row(const Params& p, int64_t token, const i
   }
 }
 
-// One workgroup a token and part of its row; every one counts all choices.
-template <class V>
+// One workgroup a token, or SEVERAL, one after the other, and part of their rows; every one counts
+// all choices.
+template <class V, bool SEVERAL>
 __global__ __launch_bounds__(kThreads) void dispatch_few(const Params p) {
   __shared__ int total[kMaxExperts], before[kMaxExperts], sums[kWaves], places[kMaxChoices];
   const int tid = threadIdx.x, k = (int)p.top_k.d;
   for (int e = tid; e < p.experts; e += kThreads) total[e] = before[e] = 0;
   __syncthreads();
-  const int own = blockIdx.x * k;  // the token's first choice
+  const int from = (int)blockIdx.x * (SEVERAL ? p.each : 1);  // the first token
+  const int to = min(from + (SEVERAL ? p.each : 1), (int)p.tokens), own = from * k;
+#pragma unroll SEVERAL ? 4 : 1
   for (int i = tid; i < p.entries; i += kThreads) {
     const int e = p.chosen[i];
     if ((uint32_t)e >= (uint32_t)p.experts) continue;
@@ -124,20 +131,26 @@ __global__ __launch_bounds__(kThreads) void dispatch_few(const Params p) {
     for (int e = tid; e < p.experts; e += kThreads) p.offsets[e] = total[e];
     if (tid == 0) p.offsets[p.experts] = all;
   }
-  if (p.entries == 0) return;
-  if (tid < k) {
-    const int e = p.chosen[own + tid];
-    int at = -1;
-    if ((uint32_t)e < (uint32_t)p.experts) {
-      at = total[e] + before[e];
-      for (int j = 0; j < tid; ++j) at += p.chosen[own + j] == e;
+  for (int t = from; t < to; ++t) {
+    if (tid < k) {
+      const int e = p.chosen[t * k + tid];
+      int at = -1;
+      if ((uint32_t)e < (uint32_t)p.experts) {
+        at = total[e] + before[e];
+        for (int j = 0; j < tid; ++j) at += p.chosen[t * k + j] == e;
+      }
+      places[tid] = at;
+      if (blockIdx.y == 0) p.place[t * k + tid] = at;
     }
-    places[tid] = at;
-    if (blockIdx.y == 0) p.place[own + tid] = at;
+    __syncthreads();
+    copy_row<V, 1, false>(p, t, places, blockIdx.y * kThreads + tid, gridDim.y * kThreads);
+    if (!SEVERAL || t + 1 == to) break;
+    if (tid < k) {
+      const int e = p.chosen[t * k + tid];
+      if ((uint32_t)e < (uint32_t)p.experts) atomicAdd(&before[e], 1);
+    }
+    __syncthreads();  // (the places have been read, too)
   }
-  __syncthreads();
-  copy_row<V, 1, false>(p, blockIdx.x, places, blockIdx.y * kThreads + tid,
-                        gridDim.y * kThreads);
 }
 
 __global__ __launch_bounds__(kThreads) void count_chunks(const Params p) {
@@ -374,15 +387,18 @@ hipError_t dispatch_launch(const DispatchArgs& a, hipStream_t stream) {
   const bool wide = a.hidden % 8 == 0 && ((uintptr_t)a.x | (uintptr_t)a.rows) % 16 == 0;
   const int64_t pieces = wide ? a.hidden / 8 : a.hidden;
   if (p.entries <= kFew) {
-    // workgroups for the chip's 256 compute units, of a piece a thread at least
-    const int64_t want = a.tokens > 0 ? (512 + a.tokens - 1) / a.tokens : 1;
+    // Up to four workgroups for each of the chip's 256 compute units, of a piece a thread at least.
+    // (With the loop over several tokens, 64 tokens of 8 rows of 7168 take 4.9 us instead of 4.7.)
+    p.each = (int32_t)std::max((a.tokens + 1023) / 1024, (int64_t)1);
+    const int64_t blocks = std::max((a.tokens + p.each - 1) / p.each, (int64_t)1);
     const int64_t most = (pieces + kThreads - 1) / kThreads;
-    const dim3 grid((uint32_t)(a.tokens > 0 ? a.tokens : 1), (uint32_t)(want < most ? want : most));
-    if (wide)
-      dispatch_few<uint4v><<<grid, kThreads, 0, stream>>>(p);
-    else
-      dispatch_few<uint16_t><<<grid, kThreads, 0, stream>>>(p);
-    return hipGetLastError();
+    const dim3 grid((uint32_t)blocks, (uint32_t)std::min((511 + blocks) / blocks, most));
+    void* kernel = p.each > 1 ? (wide ? (void*)dispatch_few<uint4v, true>
+                                      : (void*)dispatch_few<uint16_t, true>)
+                              : (wide ? (void*)dispatch_few<uint4v, false>
+                                      : (void*)dispatch_few<uint16_t, false>);
+    void* args[] = {&p};
+    return hipLaunchKernel(kernel, grid, dim3(kThreads), args, 0, stream);
   }
   count_chunks<<<p.chunks, kThreads, 0, stream>>>(p);
   place_chunks<<<p.chunks, kThreads, 0, stream>>>(p);
