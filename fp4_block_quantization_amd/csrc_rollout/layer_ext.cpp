@@ -34,7 +34,8 @@ double real(PyObject* o) {
 const at::Tensor& either(PyObject* o, const char* name, bool& fp32) {
   const at::Tensor& t = tensor(o, name);
   if (t.scalar_type() != at::kFloat && t.scalar_type() != at::kBFloat16)
-    refuse(std::string(name) + " must be bfloat16 or float32, got " + at::toString(t.scalar_type()));
+    refuse(std::string(name) + " must be bfloat16 or float32, got " +
+           at::toString(t.scalar_type()));
   fp32 = t.scalar_type() == at::kFloat;
   return t;
 }

@@ -675,10 +675,13 @@ namespace {
 // the join 4 us.  So the steps are cut in the square root of their time by a part's, up to two
 // workgroups a compute unit, where there are 12 us of them.  Measured, with 32 heads on 8 of 128
 // but for the last, whole and in 2, 4, 8 and 16 parts (the rule's number first):
-//   16 queries behind 8000 keys  (13) 130, 74, 43, 30, 27 us     64 behind 2000  (5) 42, 30, 22, 21, 26
-//   256 behind 4000               (4)  75, 48, 36, 41, 58       8 times 16 behind 1000  (2) 25, 22, 21, 25, 36
-//   512 behind 16000              (3) 260, 163, 156, 170, 209   512 behind 512  (1) 26, 26, 31, 48, 78
-//   512, 8 heads on 2 of 256, behind 4000  (7) 136, 81, 54, 44, 63
+//   16 queries behind 8000 keys  (13) 117, 67, 39, 27, 25 us
+//   64 behind 2000                (5) 37, 26, 20, 18, 23
+//   256 behind 4000               (4) 68, 45, 34, 37, 50
+//   8 times 16 behind 1000        (2) 22, 20, 19, 21, 30
+//   512 behind 16000              (3) 238, 150, 142, 154, 184
+//   512 behind 512                (1) 22, 24, 27, 42, 68
+//   512, 8 heads on 2 of 256, behind 4000  (6) 121, 76, 53, 46, 61
 int64_t parts_of(int64_t q_tokens, int64_t q_heads, int64_t k_tokens, int64_t kv_heads,
                  int64_t head_dim, int64_t batch) {
   const int64_t groups = (q_tokens * (q_heads / kv_heads) / kRows + batch) * kv_heads;
@@ -727,10 +730,16 @@ hipError_t prompt_launch(const PromptArgs& a, hipStream_t stream) {
   p.blocks = (int32_t)(a.q_tokens * p.per_head.d / kRows + a.batch);
   auto launch = [&](const void* kernel, const void* join) {
     const int64_t total = (int64_t)p.blocks * a.kv_heads * parts;
-    // The order matters where workgroups wait for others to end (two of them fit a compute unit)
-    // and there are sequences to order.  By length and by place: 4 sequences of 512 queries behind
-    // up to 8192 keys 188 and 192 us; 13 of up to 300 10.8 and 10.1, one of 512 15.4 and 14.8.
-    p.by_length = a.batch > 1 && a.batch <= 64 && total > 512;
+    // By place, numbers without a block lie between the others, and workgroups go round the compute
+    // units by number: where there are more than one each (two fit), some units have two and others
+    // none.  By length they come last, and the order is right where workgroups wait for others; but
+    // finding a block takes longer, the more sequences the longer.  By place and by length: 4 times
+    // 32 queries behind 4000 keys, in 5 parts, 34.7 and 26.8 us, 8 times 16 behind 2000, in 4, 28.1
+    // and 23.2; whole, 6 of 200 to 300 18.9 and 16.7, 20 of 20 to 80 10.9 and 11.3, 40 of 10 to 60
+    // 11.1 and 12.9; where all have a unit, 13 of up to 300 10.1 and 10.8, one of 512 14.8 and 15.4;
+    // where some wait, 4 times 512 behind up to 8192 192 and 188.
+    const int64_t alone = a.batch <= 16 ? 256 : 512;
+    p.by_length = a.batch > 1 && a.batch <= 64 && (parts > 1 || total > alone);
     const int64_t most = ((int64_t)1 << 32) / (64 * kWaves) - 1;  // (a launch holds 2^32 threads)
     void* args[] = {&p};
     hipError_t e = hipSuccess;

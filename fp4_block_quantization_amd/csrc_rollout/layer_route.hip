@@ -313,7 +313,8 @@ hipError_t route_launch(const RouteArgs& a, hipStream_t stream) {
            (int32_t)a.top_k, (int32_t)a.groups, (int32_t)a.top_groups,
            divisor_of((uint32_t)(a.experts / a.groups)), a.scale};
   const bool wide = a.bias || a.groups > 1;
-  void* kernel = a.fp32 ? (wide ? kernel_of<float, true>(a.experts) : kernel_of<float, false>(a.experts))
+  void* kernel = a.fp32 ? (wide ? kernel_of<float, true>(a.experts)
+                                : kernel_of<float, false>(a.experts))
                         : (wide ? kernel_of<__bf16, true>(a.experts)
                                 : kernel_of<__bf16, false>(a.experts));
   bool sigmoid = a.sigmoid, renormalize = a.renormalize;

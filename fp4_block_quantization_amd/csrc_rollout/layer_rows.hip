@@ -404,11 +404,11 @@ hipError_t dispatch_launch(const DispatchArgs& a, hipStream_t stream) {
   place_chunks<<<p.chunks, kThreads, 0, stream>>>(p);
   const int64_t blocks = (a.tokens + kWaves - 1) / kWaves;
   const uint32_t grid = (uint32_t)(blocks < (1 << 20) ? blocks : (1 << 20));
-  // Rows that the last-level cache does not hold go past it: what reads them next finds most of them
-  // evicted either way, and lines that are still to be written slow it down.  Dispatch and a pass
-  // that reads its rows, past the caches and through them: 67 MB 42 and 37 us, 134 MB 74 and 71,
-  // 268 MB 141 and 143, 1.9 GB 913 and 929; and a pass that reads other memory: 39 and 48, 74 and 81,
-  // 141 and 158, 915 and 929.
+  // Rows that the last-level cache does not hold go past it: what reads them next finds most of
+  // them evicted either way, and lines that are still to be written slow it down.  Dispatch and a
+  // pass that reads its rows, past the caches and through them: 67 MB 42 and 37 us, 134 MB 74 and
+  // 71, 268 MB 141 and 143, 1.9 GB 913 and 929; and a pass that reads other memory: 39 and 48, 74
+  // and 81, 141 and 158, 915 and 929.
   const bool once = (int64_t)p.entries * a.hidden * 2 >= kLastLevel;
   if (wide && once)
     copy_rows<uint4v, true><<<grid, kThreads, 0, stream>>>(p);

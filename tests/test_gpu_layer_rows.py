@@ -42,7 +42,8 @@ def check(x, e, experts, got):
     assert torch.equal(rows[at].view(torch.int16), x[torch.from_numpy(token).cuda()].view(torch.int16))
 
 
-# up to 4096 choices in one launch, more in several; passes of 1024
+# up to 8192 choices in one launch (workgroups of several tokens from 1025 on), more in several;
+# passes of 1024
 @pytest.mark.parametrize("tokens,top_k", [(1, 1), (1, 64), (3, 5), (64, 8), (511, 8), (512, 8), (513, 8), (4097, 1),
                                           (700, 6), (64, 64), (2500, 7), (20000, 2)])
 @pytest.mark.parametrize("experts", [1, 2, 31, 64, 257, 1024])
