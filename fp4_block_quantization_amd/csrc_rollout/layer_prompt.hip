@@ -736,8 +736,8 @@ hipError_t prompt_launch(const PromptArgs& a, hipStream_t stream) {
     // finding a block takes longer, the more sequences the longer.  By place and by length: 4 times
     // 32 queries behind 4000 keys, in 5 parts, 34.7 and 26.8 us, 8 times 16 behind 2000, in 4, 28.1
     // and 23.2; whole, 6 of 200 to 300 18.9 and 16.7, 20 of 20 to 80 10.9 and 11.3, 40 of 10 to 60
-    // 11.1 and 12.9; where all have a unit, 13 of up to 300 10.1 and 10.8, one of 512 14.8 and 15.4;
-    // where some wait, 4 times 512 behind up to 8192 192 and 188.
+    // 11.1 and 12.9; where all have a unit, 13 of up to 300 10.1 and 10.8, one of 512 14.8 and
+    // 15.4; where some wait, 4 times 512 behind up to 8192 192 and 188.
     const int64_t alone = a.batch <= 16 ? 256 : 512;
     p.by_length = a.batch > 1 && a.batch <= 64 && (parts > 1 || total > alone);
     const int64_t most = ((int64_t)1 << 32) / (64 * kWaves) - 1;  // (a launch holds 2^32 threads)

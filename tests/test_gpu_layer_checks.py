@@ -1,5 +1,7 @@
 """The layer operators' binding: shapes and types that are refused, gradients,
 other streams, two calls at once, and captured graphs."""
+import threading
+
 import pytest
 import torch
 
@@ -250,3 +252,39 @@ def test_small_outputs_of_a_call_share_an_allocation_and_nothing_else():
     q, k = next(calls(20000))
     assert q.untyped_storage().data_ptr() != k.untyped_storage().data_ptr()
     assert q.storage_offset() == k.storage_offset() == 0
+
+
+def test_calls_in_inference_mode_and_from_threads():
+    def chain(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x = torch.randn((130, 6, 64), generator=g, device="cuda").bfloat16()
+        f, a = fq.rotary_frequencies(64)
+        q, k = fq.rotary(x[:, :4], x[:, 4:5], torch.arange(130, device="cuda"), f, amplitude=a)
+        off = torch.tensor([0, 30, 130], dtype=torch.int32, device="cuda")
+        o, lse = fq.prompt_attention(q, k, x[:, 5:], off, lse=True)
+        w, e = fq.moe_route(o.view(130, 256).float(), 4)
+        rows, offsets, place = fq.moe_dispatch(o.view(130, 256), e, 256)
+        return q, k, o, lse, w, e, rows, offsets, place, fq.moe_combine(rows, place, w, add=o.view(130, 256))
+
+    want = [chain(i) for i in range(4)]
+    with torch.inference_mode():
+        got = chain(0)
+        assert all(t.is_inference() for t in got)
+        assert all(torch.equal(a, b) for a, b in zip(want[0], got))
+        got[0].add_(1)
+    results = [None] * 4
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                results[i] = chain(i)
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(4):
+        assert all(torch.equal(a, b) for a, b in zip(want[i], results[i]))
