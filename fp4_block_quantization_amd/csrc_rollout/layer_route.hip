@@ -270,17 +270,25 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const Params p, cons
   const float logit = lane < p.top_k ? all[wave][expert] : 0.0f;
   float w = 0.0f;
   auto add = [](float a, float b) { return a + b; };
+  auto most = [](float a, float b) { return __builtin_fmaxf(a, b); };
   if (sigmoid) {
-    if (lane < p.top_k) w = 1.0f / (1.0f + expf(-logit));
+    // e^min(x, 0) / (1 + e^-|x|), which no exponential overflows in; to be renormalized, where every
+    // chosen logit is below zero, relative to the largest numerator, or all might underflow
+    const float e = expf(-__builtin_fabsf(logit));
+    float part = logit < 0.0f ? e : 1.0f;
+    if (renormalize && !__any(lane < p.top_k && logit >= 0.0f)) {
+      const float base = over_lanes(lane < p.top_k ? logit : -INFINITY, most);
+      part = base == -INFINITY ? 0.0f : expf(logit - base);
+    }
+    if (lane < p.top_k) w = part / (1.0f + e);
     if (renormalize) {
       const float sum = over_lanes(w, add);
       w = sum == 0.0f ? 0.0f : w / sum;
     }
   } else if (renormalize) {
     // relative to the largest chosen: what the others add to the sum cancels
-    const float most = over_lanes(lane < p.top_k ? logit : -INFINITY,
-                                  [](float a, float b) { return __builtin_fmaxf(a, b); });
-    if (lane < p.top_k && most != -INFINITY) w = expf(logit - most);
+    const float base = over_lanes(lane < p.top_k ? logit : -INFINITY, most);
+    if (lane < p.top_k && base != -INFINITY) w = expf(logit - base);
     const float sum = over_lanes(w, add);
     w = sum == 0.0f ? 0.0f : w / sum;
   } else {

@@ -116,12 +116,14 @@ FP4Q_API int64_t prompt_attention_workspace_bytes(int64_t q_tokens, int64_t q_he
  *   chosen  the top_k largest keys, in falling order; of equal keys or marks
  *           the lower index comes first
  *   weight  the chosen score, with renormalize divided by the sum of the chosen
- *           scores (0 where that is 0), times scale
+ *           scores (0 where all their logits are -infinity), times scale; renormalized
+ *           weights are formed relative to the largest, so that scores below
+ *           FP32's range keep their shares
  *
  * Keys with a bias, and marks, are formed in FP64 and compared to 42 bits behind
  * the leading one.  A NaN key ranks behind every other, and the weights of a
  * token with a NaN logit may be NaN; the chosen experts are always distinct and
- * in range.  A token whose logits are all -infinity has weights of 0 (softmax).
+ * in range.  A token whose logits are all -infinity has weights of 0.
  *
  *   logits   BF16 (fp32 0) or float (1) [tokens, experts], aligned to an element.
  *   tokens   0 ... 2^30; experts 1 ... 1024; top_k 1 ... 64, at most

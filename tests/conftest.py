@@ -61,3 +61,18 @@ def olib():
 
 def fnptr(lib, name):
     return ctypes.cast(getattr(lib, name), ctypes.c_void_p)
+
+
+# Tests that hold a value which is wrong, with the reason; they run, and are expected to fail.  What
+# is right in them is tested anew in the file that the reason names.
+WRONG_VALUES = {
+    "test_gpu_layer_route.py::test_weights_that_underflow":
+        "sigmoid weights of the logits -150 and -200 are 1 and e^-50, not 0 and 0 (test_gpu_layer_route_weights.py)",
+}
+
+
+def pytest_collection_modifyitems(items):
+    for item in items:
+        reason = WRONG_VALUES.get("%s::%s" % (item.path.name, item.name))
+        if reason:
+            item.add_marker(pytest.mark.xfail(reason=reason, strict=True))
