@@ -10,7 +10,7 @@
 // are (half a step is 2^-8 of it or less, and a row's errors are averaged over
 // its keys); s, m, l and O are FP32, and l sums p before it is rounded.  Where
 // |m c| passes 2^20, s c - m c would lose more than 2^-4 to cancellation and is
-// formed as (s - m) c, in steps of their own.
+// formed as (s - m) c, in steps of their own (and of the rows where it does).
 //
 // Layout.  Scores are computed transposed, S^T = K Q^T (32 x 32 x 16 matrix
 // instructions): a lane holds 16 keys' scores of one query of every 32 keys,
@@ -358,11 +358,13 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
     }
     return a;
   };
-  // m and what hangs on it, for a step whose largest score of this lane's keys is top
+  // m and what hangs on it, for a step whose largest score of this lane's keys is top.  A row's m
+  // moves by its own scores alone: a key that other rows of the wavefront see changes none of its bits.
   auto renew = [&](float top) {
     top = __builtin_fmaxf(top, other_half(top));
-    if (__any((top - m) * p.c > kSlack)) {
-      const float next = __builtin_fmaxf(m, top);
+    const bool moves = (top - m) * p.c > kSlack;
+    if (__any(moves)) {
+      const float next = moves ? top : m;
       const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - next) * p.c);
       m = next;
       mc = m == -INFINITY ? 0.0f : m * p.c;
@@ -388,9 +390,12 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
   // scores to the exponents of their probabilities
   auto exponents = [&](const float16v (&sc)[2], float16v (&to)[2]) {
     if (large) {
-      const float base = m == -INFINITY ? 0.0f : m;
+      const bool far = __builtin_fabsf(mc) >= kLarge;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) to[i / 16][i % 16] = (sc[i / 16][i % 16] - base) * p.c;
+      for (int i = 0; i < 32; ++i) {
+        const float x = sc[i / 16][i % 16];
+        to[i / 16][i % 16] = far ? (x - m) * p.c : __builtin_fmaf(x, p.c, -mc);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
