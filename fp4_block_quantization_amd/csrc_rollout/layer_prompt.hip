@@ -724,7 +724,8 @@ hipError_t prompt_launch(const PromptArgs& a, hipStream_t stream) {
   p.kv_heads = divisor_of((uint32_t)a.kv_heads);
   p.per_head = divisor_of((uint32_t)(a.q_heads / a.kv_heads));
   const float c = __builtin_fabsf(a.scale) * kLog2e;
-  p.c = c > 0x1p-126f ? c : 0x1p-126f;  // (zero times an infinite score would be NaN)
+  // (zero times an infinite score would be NaN; this leaves less than 2^-20 of any finite one)
+  p.c = c > 0.0f ? c : 0x1p-149f;
   p.sign = a.scale < 0.0f ? 0x80008000u : 0u;
   const int64_t parts = parts_of(a.q_tokens, a.q_heads, a.k_tokens, a.kv_heads,
                                  a.head_dim, a.batch);
