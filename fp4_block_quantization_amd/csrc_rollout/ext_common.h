@@ -106,36 +106,12 @@ struct Device {
   }
 };
 
-// Outputs of a call.  Small ones lie in one allocation: each costs a microsecond of the host's time,
-// of the five that a call takes.  (Larger ones do not keep each other's memory.)
+// Outputs of a call, each in memory of its own, which costs the host a microsecond apiece: in one
+// storage, one that is resized in place, or by torch as an out=, grows over the next without a word.
 template <size_t N>
 void allocate(const Device& device, const at::IntArrayRef (&shapes)[N],
               const at::ScalarType (&types)[N], at::Tensor* out) {
-  constexpr int64_t kTogether = 4 << 20, kAlign = 256;  // bytes
-  int64_t at[N], total = 0;
-  for (size_t i = 0; i < N && total <= kTogether; ++i) {
-    int64_t bytes = (int64_t)c10::elementSize(types[i]);
-    for (int64_t n : shapes[i]) {
-      if (n > kTogether || (bytes *= n) > kTogether) {
-        bytes = kTogether + 1;
-        break;
-      }
-    }
-    at[i] = total;
-    total += (bytes + kAlign - 1) / kAlign * kAlign;
-  }
-  if (total > kTogether) {
-    for (size_t i = 0; i < N; ++i) out[i] = device.empty(shapes[i], types[i]);
-    return;
-  }
-  const at::Tensor all = device.empty({total}, at::kByte);
-  for (size_t i = 0; i < N; ++i) {
-    out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
-                                                      c10::scalarTypeToTypeMeta(types[i]));
-    c10::TensorImpl* t = out[i].unsafeGetTensorImpl();
-    t->set_sizes_contiguous(shapes[i]);
-    t->set_storage_offset(at[i] / (int64_t)c10::elementSize(types[i]));
-  }
+  for (size_t i = 0; i < N; ++i) out[i] = device.empty(shapes[i], types[i]);
 }
 
 struct Workspace {

@@ -4,8 +4,7 @@ Python binding of libfp4q_rollout.so (C ABI in include/fp4q/layer.h).
 In the manner of rollout.py: GPU tensors in, outputs allocated on the inputs'
 device or passed in, launches on torch's current stream, checks in a native
 module (csrc_rollout/layer_ext.cpp), no CPU fallback, no backward pass (in
-grad mode an input that requires a gradient is refused).  Outputs of one call
-that together take up to 4 MiB lie in one storage, apart from each other.
+grad mode an input that requires a gradient is refused).
 
   rotary_frequencies(dims, base=10000.0, method="none", ..) -> frequencies, amplitude
   rotary(q, k, positions, frequencies, amplitude=1.0) -> q, k

@@ -68,6 +68,8 @@ def fnptr(lib, name):
 WRONG_VALUES = {
     "test_gpu_layer_route.py::test_weights_that_underflow":
         "sigmoid weights of the logits -150 and -200 are 1 and e^-50, not 0 and 0 (test_gpu_layer_route_weights.py)",
+    "test_gpu_layer_checks.py::test_small_outputs_of_a_call_share_an_allocation_and_nothing_else":
+        "outputs in one storage are not apart: one that is resized grows over the next (test_gpu_layer_outputs.py)",
 }
 
 
