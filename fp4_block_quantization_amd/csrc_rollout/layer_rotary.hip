@@ -3,7 +3,10 @@
 // Mathematics.  The angle p f is reduced in FP64 to quarter turns and a rest
 // of at most an eighth of a turn either way, whose sine and cosine are their
 // Taylor polynomials (degrees 9 and 10: 2e-9 off at the ends).  FP32 would lose
-// the angle of far positions: 10^6 radians have 2^-4 as their last place there.
+// the angle of far positions: 10^6 radians have 2^-4 as their last place there.  Of
+// 2^22 quarter turns and more the low parts of the products are kept, too, in a
+// second pass (in one for all angles, 8192 tokens of 40 heads of 128 take 0.5 us
+// more, 777 of FP32 0.3).
 //
 // Work.  A thread owns some pairs of one token (16 bytes of a head, or two
 // times 16 where the halves lie apart), computes their sines and cosines once
@@ -13,6 +16,8 @@
 // 128 are 168 MB, 28.9 us, 5.8 TB/s, where a large copy reaches 5.3 to 6.4.
 // 64 tokens take 2.9 us on the device, of which a launch that does nothing is
 // 2.4.
+#include <type_traits>
+
 #include "layer_launch.h"
 #include "rollout_divisor.h"
 
@@ -23,6 +28,10 @@ constexpr int kThreads = 256;
 // Threads wanted, so that a token's angles serve few heads of many tokens: 8192 tokens of 40 heads
 // of 128 take 42.9 us with 131072, 31.3 with twice that, 29.1, and 28.4 with this many.
 constexpr int64_t kWanted = 1048576;
+
+// Quarter turns from which angles are formed once more with the low parts of their products.  Up to
+// there an angle is off by 2^-28, far behind by no small part of a turn.
+constexpr double kFar = 0x1p22;
 
 struct Params {
   const char* in[2];
@@ -44,11 +53,26 @@ struct Turn {
   float c, s;
 };
 
-__device__ __forceinline__ Turn turn_of(double position, double frequency) {
-  // 2 / pi, so that x counts quarter turns
-  const double x = position * frequency * 0.63661977236758134308;
-  const double n = __builtin_rint(x);
-  const float r = (float)((x - n) * 1.57079632679489661923);
+// Sine and cosine of position * frequency; `most` takes the largest size of x so far, whose three
+// roundings lose 2^-51 of it.  FAR: with the products' low parts.
+template <bool FAR>
+__device__ __forceinline__ Turn turn_of(double position, double frequency, double& most) {
+  // 2 / pi in two words, so that x counts quarter turns
+  constexpr double kFirst = 0.63661977236758134308, kSecond = -3.9357353350364971764e-17;
+  auto mod4 = [](double v) { return (int)(v - 4.0 * __builtin_floor(v * 0.25)); };  // (past an int)
+  const double angle = position * frequency, x = angle * kFirst, n = __builtin_rint(x);
+  double rest = x - n;
+  int quarter = mod4(n);
+  if constexpr (FAR) {
+    rest += __builtin_fma(angle, kFirst, -x) +
+            (angle * kSecond + __builtin_fma(position, frequency, -angle) * kFirst);
+    const double more = __builtin_rint(rest);  // (the low parts may be quarters, too)
+    rest -= more;
+    quarter = (quarter + mod4(more)) & 3;
+  } else {
+    most = __builtin_fmax(most, __builtin_fabs(x));
+  }
+  const float r = (float)(rest * 1.57079632679489661923);
   const float r2 = r * r;
   float s = 2.7557319223985893e-6f;  // 1 / 9!
   s = __builtin_fmaf(s, r2, -1.9841269841269841e-4f);
@@ -61,8 +85,6 @@ __device__ __forceinline__ Turn turn_of(double position, double frequency) {
   c = __builtin_fmaf(c, r2, 4.1666666666666667e-2f);
   c = __builtin_fmaf(c, r2, -0.5f);
   c = __builtin_fmaf(c, r2, 1.0f);
-  // the quarter: n mod 4 (x may be past an int)
-  const int quarter = (int)(n - 4.0 * __builtin_floor(n * 0.25));
   const bool odd = quarter & 1;
   const float a = odd ? s : c, b = odd ? c : s;
   return Turn{quarter == 1 || quarter == 2 ? -a : a, quarter >= 2 ? -b : b};
@@ -135,12 +157,17 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(const Params p) {
   float c[PAIRS], s[PAIRS];
   if (turns) {
     const double position = (double)p.positions[token];
+    double most = 0.0;
+    auto turn = [&](auto far) {
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-      const Turn t = turn_of(position, p.frequencies[unit * PAIRS + i]);
-      c[i] = t.c * p.amplitude;
-      s[i] = (INVERSE ? -t.s : t.s) * p.amplitude;
-    }
+      for (int i = 0; i < PAIRS; ++i) {
+        const Turn t = turn_of<decltype(far)::value>(position, p.frequencies[unit * PAIRS + i], most);
+        c[i] = t.c * p.amplitude;
+        s[i] = (INVERSE ? -t.s : t.s) * p.amplitude;
+      }
+    };
+    turn(std::false_type{});
+    if (most >= kFar) turn(std::true_type{});
   }
   for (int h = slot; h < all; h += (int)p.slots.d) {
     const int which = h >= p.heads[0];

@@ -31,9 +31,9 @@ extern "C" {
  * the angle a = positions[t] * frequencies[i] and scaled:
  *   (u, v) -> amplitude * (u cos a - v sin a, v cos a + u sin a)
  * and by -a with inverse = 1 (the transposed map, so also the gradient; with
- * amplitude 1 it undoes the turn).  Elements from dims on are copied.  Angles
- * are reduced in FP64, sines and cosines are within 2^-23, products are FP32,
- * rounded once to the tensors' type.
+ * amplitude 1 it undoes the turn).  Elements from dims on are copied.  Sines and
+ * cosines are those of the exact product within 2^-23, for angles up to 2^70
+ * radians; products are FP32, rounded once to the tensors' type.
  *
  *   q, k          token t's [heads, head_dim] rows at element t * stride
  *                 (a slice of a fused projection is taken as it lies);
