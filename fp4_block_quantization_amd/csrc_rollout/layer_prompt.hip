@@ -542,7 +542,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
   };
   const int own_steps = min((wave_limit + kKeys - 1) / kKeys, steps);  // this wavefront's end
   const int whole_steps = min(all_see / kKeys, steps);  // end of those that all its rows see whole
-  const int last_whole = kMaskNext ? min(whole_steps, own_steps - 1) : whole_steps - 1;
+  const int last_whole = min(whole_steps, kMaskNext ? own_steps - 1 : own_steps) - !kMaskNext;
   // (one copy of the code of each kind of step: a workgroup of few steps waits for instructions)
   // The pairs copied in the inner loop have to exist to their last key (behind the last step keys
   // are copied as well, once more the last step's, and not used).
