@@ -68,8 +68,9 @@ FP4Q_API fp4q_status rotary_embed(const void* q, int64_t q_stride, int64_t q_hea
  * log-sum-exp of -infinity; so does one whose visible scores are all
  * -infinity.  Rows outside [q_offsets[0], q_offsets[batch]) are left as they
  * are.  Scores, maxima, sums and outputs are held in FP32; probabilities
- * enter the value product in BF16, relative to the row's largest (up to 2^8
- * of an earlier largest).  Keys and values that a query does not see have no
+ * enter the value product in BF16, relative to the row's largest (up to 2^12
+ * of an earlier largest, so that 2^12 times the sum of a row's values has to
+ * stay within FP32).  Keys and values that a query does not see have no
  * effect on it, infinities and NaN among them; a value that is not finite, where
  * a query sees it, makes that element of its output infinite or NaN.
  *
