@@ -18,6 +18,9 @@ decltype(&moe_dispatch) p_moe_dispatch;
 decltype(&moe_dispatch_workspace_bytes) p_moe_dispatch_workspace_bytes;
 decltype(&moe_combine) p_moe_combine;
 
+// Sizes that outputs are allocated by, refused here before that.
+constexpr int64_t kMaxChoices = 64, kMaxExperts = 1024;
+
 int64_t integer(PyObject* o) {
   const long long v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw Raised();
@@ -207,7 +210,8 @@ PyObject* route(PyObject* const* arg) {
     device.same(t);
     active = (const uint8_t*)t.const_data_ptr();
   }
-  if (top_k < 1) refuse("top_k must be at least 1");
+  if (top_k < 1 || top_k > kMaxChoices)
+    refuse("top_k must be 1 to " + std::to_string(kMaxChoices));
   at::Tensor out[2];
   if (arg[9] == Py_None) {
     const int64_t shape[] = {tokens, top_k};
@@ -237,7 +241,8 @@ PyObject* dispatch(PyObject* const* arg) {
   if (chosen.dim() != 2 || chosen.size(0) != x.size(0)) refuse("experts must be [tokens, top_k]");
   const int64_t tokens = x.size(0), hidden = x.size(1), top_k = chosen.size(1);
   const int64_t experts = integer(arg[2]);
-  if (experts < 1) refuse("num_experts must be at least 1");
+  if (experts < 1 || experts > kMaxExperts)
+    refuse("num_experts must be 1 to " + std::to_string(kMaxExperts));
   const Device device(x);
   device.same(chosen);
   at::Tensor out[3];
