@@ -351,6 +351,13 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const Sums p) {
   }
 }
 
+// The launch's own error: hipGetLastError would report, and clear, what another call has left.
+template <class P>
+hipError_t launch(void* kernel, dim3 grid, P p, hipStream_t stream) {
+  void* args[] = {&p};
+  return hipLaunchKernel(kernel, grid, dim3(kThreads), args, 0, stream);
+}
+
 struct Chunks {
   int64_t count, each;
 };
@@ -397,11 +404,11 @@ hipError_t dispatch_launch(const DispatchArgs& a, hipStream_t stream) {
                                       : (void*)dispatch_few<uint16_t, true>)
                               : (wide ? (void*)dispatch_few<uint4v, false>
                                       : (void*)dispatch_few<uint16_t, false>);
-    void* args[] = {&p};
-    return hipLaunchKernel(kernel, grid, dim3(kThreads), args, 0, stream);
+    return launch(kernel, grid, p, stream);
   }
-  count_chunks<<<p.chunks, kThreads, 0, stream>>>(p);
-  place_chunks<<<p.chunks, kThreads, 0, stream>>>(p);
+  hipError_t e = launch((void*)count_chunks, p.chunks, p, stream);
+  if (e == hipSuccess) e = launch((void*)place_chunks, p.chunks, p, stream);
+  if (e != hipSuccess) return e;
   const int64_t blocks = (a.tokens + kWaves - 1) / kWaves;
   const uint32_t grid = (uint32_t)(blocks < (1 << 20) ? blocks : (1 << 20));
   // Rows that the last-level cache does not hold go past it: what reads them next finds most of
@@ -410,13 +417,10 @@ hipError_t dispatch_launch(const DispatchArgs& a, hipStream_t stream) {
   // 71, 268 MB 141 and 143, 1.9 GB 913 and 929; and a pass that reads other memory: 39 and 48, 74
   // and 81, 141 and 158, 915 and 929.
   const bool once = (int64_t)p.entries * a.hidden * 2 >= kLastLevel;
-  if (wide && once)
-    copy_rows<uint4v, true><<<grid, kThreads, 0, stream>>>(p);
-  else if (wide)
-    copy_rows<uint4v, false><<<grid, kThreads, 0, stream>>>(p);
-  else
-    copy_rows<uint16_t, false><<<grid, kThreads, 0, stream>>>(p);
-  return hipGetLastError();
+  void* kernel = !wide  ? (void*)copy_rows<uint16_t, false>
+                 : once ? (void*)copy_rows<uint4v, true>
+                        : (void*)copy_rows<uint4v, false>;
+  return launch(kernel, grid, p, stream);
 }
 
 hipError_t combine_launch(const CombineArgs& a, hipStream_t stream) {
@@ -435,13 +439,10 @@ hipError_t combine_launch(const CombineArgs& a, hipStream_t stream) {
   auto go = [&](auto t, auto o) {
     using T = decltype(t);
     using O = decltype(o);
-    if (wide && once)
-      combine_kernel<T, O, 8, true><<<grid, kThreads, 0, stream>>>(p);
-    else if (wide)
-      combine_kernel<T, O, 8, false><<<grid, kThreads, 0, stream>>>(p);
-    else
-      combine_kernel<T, O, 1, false><<<grid, kThreads, 0, stream>>>(p);
-    return hipGetLastError();
+    void* kernel = !wide  ? (void*)combine_kernel<T, O, 1, false>
+                   : once ? (void*)combine_kernel<T, O, 8, true>
+                          : (void*)combine_kernel<T, O, 8, false>;
+    return launch(kernel, grid, p, stream);
   };
   if (a.y_fp32) return a.out_fp32 ? go(0.0f, 0.0f) : go(0.0f, __bf16{});
   return a.out_fp32 ? go(__bf16{}, 0.0f) : go(__bf16{}, __bf16{});
