@@ -86,7 +86,6 @@ def rotary_frequencies(dims, base=10000.0, method="none", factor=1.0, original_p
     elif method == "base":
         if dims == 2:
             raise Fp4qError('method "base" needs more than one pair')
-        base = base * factor ** (dims / (dims - 2.0))
     elif method == "parts":
         if original_positions is None or original_positions <= 0 or not slow < fast:
             raise Fp4qError('method "parts" needs original_positions, and slow below fast')
@@ -94,10 +93,17 @@ def rotary_frequencies(dims, base=10000.0, method="none", factor=1.0, original_p
     elif method != "none":
         raise Fp4qError('method must be "none", "positions", "base" or "parts", got %r' % (method,))
     out = []
-    for i in range(dims // 2):
-        f = base ** (-2.0 * i / dims)
-        share = 0.0 if kept is None else min(max((f * kept - slow) / (fast - slow), 0.0), 1.0)
-        out.append(f * share + f / divided * (1.0 - share))
+    try:
+        if method == "base":
+            base = base * factor ** (dims / (dims - 2.0))
+        for i in range(dims // 2):
+            f = base ** (-2.0 * i / dims)
+            share = 0.0 if kept is None else min(max((f * kept - slow) / (fast - slow), 0.0), 1.0)
+            out.append(f * share + f / divided * (1.0 - share))
+    except (OverflowError, ZeroDivisionError):
+        out = [math.inf]
+    if not all(map(math.isfinite, out)):
+        raise Fp4qError("these arguments do not give finite frequencies")
     if amplitude is None:
         amplitude = 0.1 * math.log(factor) + 1.0 if method == "parts" else 1.0
     return torch.tensor(out, dtype=torch.float64, device=device), float(amplitude)
