@@ -4,15 +4,19 @@
 // Mathematics.  With c = |scale| log2(e) (queries take the scale's sign) and m
 // a row's running maximum of its scores s:
 //   p = 2^(s c - m c), l += p, O += p v;  out = O / l, lse = (m c + log2 l) ln 2
-// m is moved only when a score passes it by 12 / c: until then p is at most
-// 2^12, and BF16 holds that as well as 1, while a move costs a pass over O (of
-// all rows of a wavefront, each of which moves for its own scores: with 8 / c
-// 4096 tokens of heads of 256 take 306 us instead of 291).  p
-// enters the value product in BF16, as the operands of the matrix instruction
+// p enters the value product in BF16, as the operands of the matrix instruction
 // are (half a step is 2^-8 of it or less, and a row's errors are averaged over
-// its keys); s, m, l and O are FP32, and l sums p before it is rounded.  Where
-// |m c| passes 2^20, s c - m c would lose more than 2^-4 to cancellation and is
-// formed as (s - m) c, in steps of their own (and of the rows where it does).
+// its keys); s, m, l and O are FP32.  l sums p as it is rounded, so that a row's
+// weights add up to one: 512 tokens are off by 0.0018 of their size, 0.0017 of it
+// the result's own rounding, and by 0.0020 with the sum of p before rounding.
+// The log-sum-exp takes that one, which is kept where it is asked for (8192
+// tokens 511 us without, 530 with it).
+// m is moved only when a score passes it by 12 / c: until then p is at most
+// 2^12, and BF16 holds that as well as 1, while a move costs a pass over O, of
+// all rows of a wavefront, each of which moves for its own scores: with 8 / c
+// 4096 tokens of heads of 256 take 314 us instead of 299.
+// Where |m c| passes 2^20, s c - m c would lose more than 2^-4 to cancellation
+// and is formed as (s - m) c, in steps of their own (and of the rows where it does).
 //
 // Layout.  Scores are computed transposed, S^T = K Q^T (32 x 32 x 16 matrix
 // instructions): a lane holds 16 keys' scores of one query of every 32 keys,
@@ -54,6 +58,7 @@
 // block after the other 524 (and the 16 sequences 257 for 240).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "layer_launch.h"
 #include "rollout_divisor.h"
@@ -91,7 +96,8 @@ struct Params {
   int32_t by_length;  // the order of the blocks
   Divisor parts;     // that a block's steps are cut into
   float* part_o;     // [parts][q_tokens][q_heads][D], where there are several
-  float2* part_ml;
+  float2* part_ml;   // m and l of each, and l before rounding
+  float* part_sum;
   uint32_t first_block;
   float c;           // |scale| log2(e)
   uint32_t sign;     // 0x80008000 for a negative scale
@@ -191,6 +197,13 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// sum + both of w's BF16 numbers.
+__device__ __forceinline__ float add_pair(float sum, uint32_t w) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 ones = {(__bf16)1.0f, (__bf16)1.0f};
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), ones, sum, false);
+}
+
 // The places of a row's 16-byte pieces are exchanged so that no two lanes of a read meet in a
 // bank.  LDS has 64 banks of 4 bytes: 16 lanes read 16 bytes each, of 16 neighbouring keys at the
 // same place, at once; these have to lie differently in 256 bytes.  A transposing read takes 8
@@ -209,7 +222,8 @@ struct Tiles {  // one step's in use, the next one's in flight
   alignas(16) uint8_t v[2][kKeys * D * 2];
 };
 
-template <int D>
+// LSE: probabilities are summed before they are rounded as well, for the log-sum-exp.
+template <int D, bool LSE>
 __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(const Params p) {
   // whether the next step's scores may be masked where they are computed beside the values'
   // product (heads of 256 have no registers for it: 583 us instead of 331 for 4096 tokens)
@@ -327,7 +341,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
   float16v o[DT];
 #pragma unroll
   for (int i = 0; i < DT; ++i) o[i] = (float16v)0.0f;
-  float m = -INFINITY, mc = 0.0f, l = 0.0f;
+  float m = -INFINITY, mc = 0.0f, l = 0.0f, sum = 0.0f;  // (sum: l before rounding)
   bool large = false, any_dirty = false;
 
   // where this lane's keys and values lie
@@ -371,6 +385,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
       m = next;
       mc = m == -INFINITY ? 0.0f : m * p.c;
       l *= f;
+      if constexpr (LSE) sum *= f;
 #pragma unroll
       for (int i = 0; i < DT; ++i) o[i] *= f;
       large = __any(__builtin_fabsf(mc) >= kLarge);
@@ -418,17 +433,26 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
     renew(largest(sc));
     exponents(sc, sc);
   };
+  // The i-th of a step's probabilities and the next one, rounded: the i / 2-th word of the weights.
+  auto weigh = [&](const float16v (&sc)[2], int i, uint4v (&weights)[4]) {
+    const float a = sc[i / 16][i % 16], b = sc[i / 16][i % 16 + 1];
+    weights[i / 8][i % 8 / 2] = pack(a, b);
+    if constexpr (LSE) {
+      sum += a;
+      sum += b;
+    }
+  };
   // a step's probabilities, from their exponents, and their product with the values
   auto add_values = [&](int step, float16v (&sc)[2]) {
     const uint8_t* t = tiles.v[step & 1];
 #pragma unroll
     for (int i = 0; i < 32; ++i) sc[i / 16][i % 16] = __builtin_amdgcn_exp2f(sc[i / 16][i % 16]);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) l += sc[i / 16][i % 16];
     uint4v weights[4];  // 16 keys each
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      weights[i / 4][i % 4] = pack(sc[i / 8][i % 8 * 2], sc[i / 8][i % 8 * 2 + 1]);
+    for (int i = 0; i < 32; i += 2) {
+      weigh(sc, i, weights);
+      l = add_pair(l, weights[i / 8][i % 8 / 2]);
+    }
     auto product = [&](auto clean) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -476,10 +500,9 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
     const uint8_t *kt = tiles.k[(step + 1) & 1], *vt = tiles.v[step & 1];
     uint4v weights[4];
     auto packed = [&](int i) {  // (a pair later: what follows an exponential at once waits for it)
-      const float a = sc[i / 16][i % 16], b = sc[i / 16][i % 16 + 1];
-      l += a;
-      l += b;
-      weights[i / 8][i % 8 / 2] = pack(a, b);
+      weigh(sc, i, weights);
+      if (i > 0) l = add_pair(l, weights[(i - 2) / 8][(i - 2) % 8 / 2]);  // (another pair later)
+      if (i == 30) l = add_pair(l, weights[3][3]);
     };
     auto probability = [&](int i) {
       const float x = __builtin_amdgcn_exp2f(sc[i / 16][i % 16]);
@@ -599,11 +622,13 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
   }
 
   l += other_half(l);
+  if constexpr (LSE) sum += other_half(sum);
   if (first + col >= rows) return;
   const int64_t row = (int64_t)(s.q0 + token) * p.q_heads + head;
   if (p.parts.d > 1) {
     const int64_t at_part = part * (int64_t)p.q_tokens * p.q_heads + row;
     if (half == 0) p.part_ml[at_part] = make_float2(m, l);
+    if (LSE && half == 0) p.part_sum[at_part] = sum;
     if (l == 0.0f) return;
     float* to = p.part_o + at_part * D + 4 * half;
 #pragma unroll
@@ -633,8 +658,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void prompt_kernel(c
       }
       *(uint4v*)(to + d * 32 + i * 8) = u;
     }
-  if (p.lse && half == 0)
-    p.lse[row] = l == 0.0f ? -INFINITY : (mc + __builtin_amdgcn_logf(l)) * kLn2;
+  if (LSE && half == 0)
+    p.lse[row] = l == 0.0f ? -INFINITY : (mc + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 // The parts of a row to its output, in order.  A wavefront takes a row, a lane D / 64 elements.
@@ -655,12 +680,13 @@ __global__ __launch_bounds__(256) void prompt_join(const Params p) {
     const float2 ml = p.part_ml[i * all + row];
     if (ml.y != 0.0f) top = __builtin_fmaxf(top, ml.x);
   }
-  float l = 0.0f, o[E] = {};
+  float l = 0.0f, sum = 0.0f, o[E] = {};
   for (int i = 0; i < parts; ++i) {
     const float2 ml = p.part_ml[i * all + row];
     if (ml.y == 0.0f) continue;  // (nothing was written)
     const float f = __builtin_amdgcn_exp2f((ml.x - top) * p.c);
     l = __builtin_fmaf(ml.y, f, l);
+    if (p.lse) sum = __builtin_fmaf(p.part_sum[i * all + row], f, sum);
     const float* from = p.part_o + (i * all + row) * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(from[e], f, o[e]);
@@ -670,7 +696,7 @@ __global__ __launch_bounds__(256) void prompt_join(const Params p) {
   for (int e = 0; e < E; ++e)
     p.out[row * D + lane * E + e] = (uint16_t)(pack(o[e] * each, 0.0f) & 0xffffu);
   if (p.lse && lane == 0)
-    p.lse[row] = l == 0.0f ? -INFINITY : (top * p.c + __builtin_amdgcn_logf(l)) * kLn2;
+    p.lse[row] = l == 0.0f ? -INFINITY : (top * p.c + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 }  // namespace
@@ -704,7 +730,7 @@ int64_t parts_of(int64_t q_tokens, int64_t q_heads, int64_t k_tokens, int64_t kv
 int64_t prompt_workspace_bytes(int64_t q_tokens, int64_t q_heads, int64_t k_tokens,
                                int64_t kv_heads, int64_t head_dim, int64_t batch) {
   const int64_t parts = parts_of(q_tokens, q_heads, k_tokens, kv_heads, head_dim, batch);
-  return parts == 1 ? 0 : parts * q_tokens * q_heads * (head_dim + 2) * 4;
+  return parts == 1 ? 0 : parts * q_tokens * q_heads * (head_dim + 3) * 4;
 }
 
 hipError_t prompt_launch(const PromptArgs& a, hipStream_t stream) {
@@ -733,8 +759,11 @@ hipError_t prompt_launch(const PromptArgs& a, hipStream_t stream) {
                                  a.head_dim, a.batch);
   p.parts = divisor_of((uint32_t)parts);
   p.part_o = (float*)a.workspace;
-  if (parts > 1)
-    p.part_ml = (float2*)(p.part_o + parts * a.q_tokens * a.q_heads * a.head_dim);
+  if (parts > 1) {
+    const int64_t all = parts * a.q_tokens * a.q_heads;
+    p.part_ml = (float2*)(p.part_o + all * a.head_dim);
+    p.part_sum = (float*)(p.part_ml + all);
+  }
   p.blocks = (int32_t)(a.q_tokens * p.per_head.d / kRows + a.batch);
   auto launch = [&](const void* kernel, const void* join) {
     const int64_t total = (int64_t)p.blocks * a.kv_heads * parts;
@@ -761,11 +790,16 @@ hipError_t prompt_launch(const PromptArgs& a, hipStream_t stream) {
                           0, stream);
     return e;
   };
+  auto sized = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    return launch(a.lse ? (void*)prompt_kernel<D, true> : (void*)prompt_kernel<D, false>,
+                  (void*)prompt_join<D>);
+  };
   switch (a.head_dim) {
-    case 64: return launch((void*)prompt_kernel<64>, (void*)prompt_join<64>);
-    case 128: return launch((void*)prompt_kernel<128>, (void*)prompt_join<128>);
-    case 192: return launch((void*)prompt_kernel<192>, (void*)prompt_join<192>);
-    default: return launch((void*)prompt_kernel<256>, (void*)prompt_join<256>);
+    case 64: return sized(std::integral_constant<int, 64>{});
+    case 128: return sized(std::integral_constant<int, 128>{});
+    case 192: return sized(std::integral_constant<int, 192>{});
+    default: return sized(std::integral_constant<int, 256>{});
   }
 }
 

@@ -70,7 +70,8 @@ FP4Q_API fp4q_status rotary_embed(const void* q, int64_t q_stride, int64_t q_hea
  * are.  Scores, maxima, sums and outputs are held in FP32; probabilities
  * enter the value product in BF16, relative to the row's largest (up to 2^12
  * of an earlier largest, so that 2^12 times the sum of a row's values has to
- * stay within FP32).  Keys and values that a query does not see have no
+ * stay within FP32), and are divided by their sum as rounded; the log-sum-exp
+ * takes them before rounding.  Keys and values that a query does not see have no
  * effect on it, infinities and NaN among them; a value that is not finite, where
  * a query sees it, makes that element of its output infinite or NaN.
  *
