@@ -38,20 +38,22 @@
 // kernel (parts_of).
 //
 // Bounds.  A step of 32 rows by 64 keys of 128 is 32 matrix instructions of 32
-// cycles and, of every lane, 32 scores at about 22 cycles of vector work (an
-// exponential is 8), 48 reads of LDS and some 90 scalar instructions.  `both`
+// cycles and, of every lane, 32 scores at about 20 cycles of vector work (an
+// exponential is 8), 48 reads of LDS and some 100 scalar instructions.  `both`
 // places them beside one another by hand.  Counted for one sequence of 8192
-// tokens, 32 heads on 8 of 128 (507 to 525 us by card, 1085 to 1050 TFLOP/s, at
-// 1.8 GHz, which power leaves; a large product of the library reaches 1380): a
-// SIMD's matrix unit works 58% of the time, its vector unit 52, the LDS 58, and
-// some instruction starts in 80: with two wavefronts a SIMD it is the starts
-// that bound.  There is one copy of the code of each kind of step, for a
+// tokens, 32 heads on 8 of 128 (502 to 522 us by card, 1095 to 1050 TFLOP/s, at
+// 1.8 GHz, which power leaves; a large product of the library reaches 1420 to
+// 1470): a SIMD's matrix unit works 58% of the time, its vector unit 48, the LDS
+// 58, and some instruction starts in 76: with two wavefronts a SIMD it is the
+// starts that bound.  (Heads of 192 and 256 have moves between the two halves of
+// the registers in that loop as well, 64 and 294 a step, and 256 spills 11;
+// heads of 64 have 169 registers, for two wavefronts a SIMD.)  There is one copy of the code of each kind of step, for a
 // workgroup of few steps waits for its instructions from memory: 16 sequences
 // of up to 2048 tokens took 273 us with the steps written out, and take 240 now
 // (800 TFLOP/s).  There four tenths of a workgroup's time go outside whole
 // steps: its block's search, the first copies and the queries, three steps one
 // after the other, the output.
-// Measured and not taken, for 8192 tokens when this took 530 us: 64 rows a
+// Measured and not taken, for 8192 tokens when this took 526 to 539 us: 64 rows a
 // wavefront 615 us (its accumulators pass through the other half of the
 // registers), two wavefronts that share rows and take every other step 635,
 // three steps' copies in flight 695; at 508, workgroups that stay and take one
@@ -715,6 +717,9 @@ namespace {
 //   512 behind 16000              (3) 238, 150, 142, 154, 184
 //   512 behind 512                (1) 22, 24, 27, 42, 68
 //   512, 8 heads on 2 of 256, behind 4000  (6) 121, 76, 53, 46, 61
+// The lengths are on the device; what the host knows is how many rows of keys there are.  Where most
+// are in no sequence there are too many parts: 16 queries behind 100 keys take 25 us in a buffer of
+// 131072 rows (55 parts) and 8 with its first 100 alone; behind 2000 of 32768 21 and 15.
 int64_t parts_of(int64_t q_tokens, int64_t q_heads, int64_t k_tokens, int64_t kv_heads,
                  int64_t head_dim, int64_t batch) {
   const int64_t groups = (q_tokens * (q_heads / kv_heads) / kRows + batch) * kv_heads;

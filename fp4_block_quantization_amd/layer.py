@@ -4,7 +4,8 @@ Python binding of libfp4q_rollout.so (C ABI in include/fp4q/layer.h).
 In the manner of rollout.py: GPU tensors in, outputs allocated on the inputs'
 device or passed in, launches on torch's current stream, checks in a native
 module (csrc_rollout/layer_ext.cpp), no CPU fallback, no backward pass (in
-grad mode an input that requires a gradient is refused).
+grad mode an input that requires a gradient is refused).  An out= must not
+overlap an input or another output, but where its call says so.
 
   rotary_frequencies(dims, base=10000.0, method="none", ..) -> frequencies, amplitude
   rotary(q, k, positions, frequencies, amplitude=1.0) -> q, k
@@ -129,8 +130,9 @@ def prompt_attention(q, k, v, q_offsets, k_offsets=None, scale=None, lse=False, 
     [q_offsets[b], q_offsets[b + 1]) and the keys [k_offsets[b], k_offsets[b +
     1]) (int32 GPU tensors [sequences + 1]; k_offsets None: q_offsets); its
     queries are the last of its keys.  So it takes whole prompts, and chunks
-    behind a context that nvfp4_kv_read has read back.  scale: default
-    1/sqrt(head_dim).  head_dim 64, 128, 192 or 256.  Rows outside the
+    behind a context that nvfp4_kv_read has read back; of a longer buffer of keys
+    pass the rows in use, by which long contexts are cut into parts.  scale:
+    default 1/sqrt(head_dim).  head_dim 64, 128, 192 or 256.  Rows outside the
     sequences are left as they are (out=).  lse=True returns (out, log-sum-exp
     f32 [tokens, heads]) as well."""
     return (_ext or _native()).prompt(q, k, v, q_offsets, k_offsets, scale, lse, out, workspace)
@@ -168,5 +170,5 @@ def moe_combine(y, place, weights, add=None, out_dtype=None, out=None):
     (BF16 [tokens, n], optional) + the sum over j of weights[t, j] * y[place[t,
     j]], summed in FP32.  A place outside y adds nothing.  out_dtype: bfloat16
     (default) or float32; out: optional [tokens, n] of either, whose type
-    decides."""
+    decides; a BF16 one may be add."""
     return (_ext or _native()).combine(y, place, weights, add, _fp32(out_dtype, out), out)

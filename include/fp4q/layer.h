@@ -66,19 +66,22 @@ FP4Q_API fp4q_status rotary_embed(const void* q, int64_t q_stride, int64_t q_hea
  * n - m + i (none, if that is negative).  Query head h reads key head
  * h / (q_heads / kv_heads).  A query that sees nothing gives zeros, and a
  * log-sum-exp of -infinity; so does one whose visible scores are all
- * -infinity.  Rows outside [q_offsets[0], q_offsets[batch]) are left as they
+ * -infinity, where the values it sees are finite.  Rows outside [q_offsets[0], q_offsets[batch]) are left as they
  * are.  Scores, maxima, sums and outputs are held in FP32; probabilities
  * enter the value product in BF16, relative to the row's largest (up to 2^12
  * of an earlier largest, so that 2^12 times the sum of a row's values has to
  * stay within FP32), and are divided by their sum as rounded; the log-sum-exp
  * takes them before rounding.  Keys and values that a query does not see have no
- * effect on it, infinities and NaN among them; a value that is not finite, where
- * a query sees it, makes that element of its output infinite or NaN.
+ * effect on any bit of it, infinities and NaN among them; a value that is not
+ * finite, where a query sees it with a score above -infinity, makes that element
+ * of its output infinite or NaN (with one of -infinity, that or nothing).
  *
  *   q            BF16: token t's [q_heads, head_dim] rows at element t * q_stride.
  *   k, v         BF16 [.., kv_heads, head_dim] rows likewise.  16-byte aligned,
  *                strides multiples of 8, at least heads * head_dim, up to 2^24.
- *   q_tokens     rows of q (and out), k_tokens rows of k and v: 0 ... 2^30.
+ *   q_tokens     rows of q (and out), k_tokens rows of k and v: 0 ... 2^30.  Keys
+ *                are cut into parts by k_tokens / batch, so of a long buffer
+ *                pass the rows in use.
  *   q_heads      a positive multiple of kv_heads (up to 65535); head_dim 64,
  *                128, 192 or 256; q_tokens * (q_heads / kv_heads) and
  *                q_tokens * q_heads / 32 + batch * kv_heads below 2^31.

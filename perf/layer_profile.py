@@ -107,7 +107,7 @@ def print_sizes(only):
         states = states_of(case)
         us = device_us(torch, lambda i: ops.run(states[i % STATES]))
         work = ops.work(case)
-        floor = max(work["bytes"] / 6.42e6, work["flops"] / 1.381e9)
+        floor = max(work["bytes"] / 6.42e6, work["flops"] / 1.47e9)
         print("| %s | %.2f | %.1f |" % (case["name"], us, floor), flush=True)
         del states
         torch.cuda.empty_cache()
