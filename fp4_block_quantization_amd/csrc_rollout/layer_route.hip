@@ -9,6 +9,8 @@
 // turned round, stands in the bits below, so that the largest is the best
 // expert, the lowest of equal ones.  Groups' marks are sums of two FP64
 // numbers for the same reason.
+// Weights decide nothing and are formed in FP32: they are off by 6e-8 of their
+// size, 3e-8 of it their own rounding.
 //
 // Work.  One wavefront takes a token; a lane holds the experts lane, lane +
 // 64, and so on.  The best are taken one at a time: a maximum over the lane's
